@@ -13,6 +13,10 @@ import os
 
 import torch
 
+from .decode import (MAX_BEAMS, MAX_CANDIDATES, MAX_POOLS, SV_ERR_LENGTH, SV_ERR_PAGE, SV_ERR_PAGES, SV_ERR_PARENT,
+                     SV_ERR_SCORE, BeamReorder, BeamSelector, CacheCommit, CacheCompact, CacheExtend, PagedCache,
+                     beam_reorder, beam_select, bind_library, cache_commit, cache_compact, cache_extend)
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libspecverify.so")
 
@@ -36,7 +40,9 @@ MAX_TREE_NODES = 128
 EXPORTED = ("spec_verify", "spec_verify_ragged", "spec_verify_workspace_size", "spec_verify_row_stats",
             "spec_verify_uniforms", "spec_verify_stream_probe", "spec_verify_outcomes",
             "spec_verify_outcomes_workspace_size", "spec_verify_tree", "spec_verify_status_str",
-            "spec_verify_noalloc", "spec_verify_noalloc_max_scratch")
+            "spec_verify_noalloc", "spec_verify_noalloc_max_scratch",
+            "spec_beam_select", "spec_beam_select_workspace_size", "spec_beam_reorder",
+            "spec_beam_reorder_paged", "spec_cache_extend", "spec_cache_commit", "spec_cache_compact")
 MAX_OUTCOME_F = 32
 
 
@@ -93,6 +99,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.spec_verify_noalloc_max_scratch.restype = sz
     lib.spec_verify_status_str.argtypes = [i32]
     lib.spec_verify_status_str.restype = ctypes.c_char_p
+    bind_library(lib)
     _lib = lib
     return lib
 
@@ -150,13 +157,16 @@ class Verifier:
     diagnostics p_target, p_draft, residual_mass, draft_conf and error_word
     are written too (error_word is cleared before every call).  draft_len, a
     [B] int32 tensor, gives ragged draft lengths K_b <= K
-    (spec_verify_ragged).
+    (spec_verify_ragged).  With a PagedCache as `cache`, whose last extend
+    reserved the step's tokens (the one it starts from and the drafts), every
+    call also commits what it accepted (spec_cache_commit).
     """
 
     def __init__(self, target: torch.Tensor, draft: torch.Tensor | None, tokens: torch.Tensor,
                  temperature, beta: float = 1.0, *, workspace: torch.Tensor | None = None,
                  accepted_len: torch.Tensor | None = None, out_tokens: torch.Tensor | None = None,
-                 aux: bool = False, stream=None, draft_len: torch.Tensor | None = None):
+                 aux: bool = False, stream=None, draft_len: torch.Tensor | None = None,
+                 cache: PagedCache | None = None):
         if target.dim() != 3:
             raise ValueError("target must be [B, K+1, V]")
         B, K1, V = target.shape
@@ -212,6 +222,7 @@ class Verifier:
         self._mid = (_ptr(temperature), ctypes.c_float(float(beta)), _ptr(accepted_len),
                      _ptr(out_tokens), _ptr(workspace), workspace.numel())
         self._stream = _stream(stream)
+        self._commit = None if cache is None else cache.committer(accepted_len, stream=stream)
 
     def __call__(self, seed: int, pass_events=None):
         """Enqueue one verify step with this Philox seed; returns
@@ -230,6 +241,8 @@ class Verifier:
         use_aux = self.aux is not None or pass_events is not None
         _check(self._fn(*self._head, int(seed) & (2**64 - 1), *self._mid,
                         ctypes.byref(aux) if use_aux else None, self._stream))
+        if self._commit is not None:
+            self._commit()
         if self.aux is not None:
             return self.accepted_len, self.out_tokens, self.aux
         return self.accepted_len, self.out_tokens
@@ -419,10 +432,13 @@ class TreeVerifier:
     temperature is 0), parent and tokens [B, N] int32 (parent[i] in
     [-1, i-1]), temperature a float or [B] float32 tensor.  Each call returns
     (accepted_len [B], out_tokens [B, N+1], path [B, N], error_word [1]);
-    error_word is cleared before every call."""
+    error_word is cleared before every call.  With a PagedCache as `cache`,
+    whose last extend reserved the root's token and the N nodes', every call
+    also moves the accepted path's rows of `pools` (CacheCompact) behind the
+    root's and commits them."""
 
     def __init__(self, target: torch.Tensor, draft: torch.Tensor | None, parent: torch.Tensor,
-                 tokens: torch.Tensor, temperature, *, stream=None):
+                 tokens: torch.Tensor, temperature, *, stream=None, cache: PagedCache | None = None, pools=None):
         if target.dim() != 3 or not target.is_contiguous():
             raise ValueError("target must be a contiguous [B, N+1, V] tensor")
         B, N1, V = target.shape
@@ -447,6 +463,13 @@ class TreeVerifier:
         self._tail = (_ptr(temperature), _ptr(self.accepted_len), _ptr(self.out_tokens), _ptr(self.path),
                       _ptr(self.error_word))
         self._stream = _stream(stream)
+        if pools is not None and cache is None:
+            raise ValueError("pools go with a cache")
+        self._after = []
+        if cache is not None:
+            if pools is not None:
+                self._after.append(cache.compactor(pools, self.path, self.accepted_len, stream=stream))
+            self._after.append(cache.committer(self.accepted_len, stream=stream))
 
     def __call__(self, seed: int, pass_events=None):
         self.error_word.zero_()
@@ -455,6 +478,8 @@ class TreeVerifier:
             b_ev, e_ev = pass_events[0].cuda_event, pass_events[1].cuda_event
         _check(load_library().spec_verify_tree(*self._head, int(seed) & (2**64 - 1), *self._tail, b_ev,
                                                e_ev, self._stream))
+        for call in self._after:
+            call()
         return self.accepted_len, self.out_tokens, self.path, self.error_word
 
 

@@ -7,9 +7,11 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SOURCES = [os.path.join(HERE, "csrc", f) for f in ("sv_api.hip", "sv_verify.hip", "sv_outcome.hip", "sv_tree.hip")]
-HEADERS = [os.path.join(HERE, "csrc", f) for f in ("sv_device.h", "sv_internal.h", "sv_accept.h", "sv_tile.h", "sv_stream.h")] + [
-    os.path.join(ROOT, "include", "specverify.h")]
+SOURCES = [os.path.join(HERE, "csrc", f) for f in ("sv_api.hip", "sv_verify.hip", "sv_outcome.hip", "sv_tree.hip",
+                                                "sv_beam.hip", "sv_move.hip", "sv_cache.hip")]
+HEADERS = [os.path.join(HERE, "csrc", f) for f in ("sv_device.h", "sv_internal.h", "sv_accept.h", "sv_tile.h", "sv_stream.h",
+                                                "sv_sort.h")] + [
+    os.path.join(ROOT, "include", "specverify.h"), os.path.join(ROOT, "include", "specdecode.h")]
 LIB = os.path.join(HERE, "libspecverify.so")
 
 HIPCC_FLAGS = [

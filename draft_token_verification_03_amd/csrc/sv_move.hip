@@ -1,0 +1,401 @@
+// sv_move.hip -- rows of caches that change places: the beams of a beam
+// search (dense caches and block tables) and the accepted path of a token
+// tree.  Copies bound by memory, done in place without a second buffer: one
+// thread owns one vector column of all rows that exchange contents, so it
+// has read every source before it writes, and no two threads touch the same
+// bytes.
+#include <algorithm>
+
+#include "specdecode.h"
+#include "sv_internal.h"
+
+namespace sv {
+
+constexpr int kMovePools = 128;  // pools per launch: their addresses travel as kernel arguments
+
+struct MoveArgs {
+    char *pool[kMovePools];
+    const int32_t *table;     // block tables, or null for dense caches
+    const int32_t *parent;    // reorder
+    const int32_t *start, *length;
+    const int32_t *path, *accepted;  // compact
+    int32_t *error_word;
+    int32_t B, W, G, S;       // S: positions per beam (dense) or per page
+    int32_t row_vecs;         // vectors per row
+    int32_t num_pages, max_blocks, max_length;
+    int32_t N, first;
+    int32_t chunks;           // workgroups per (pool, sequence, group)
+};
+
+__device__ __forceinline__ void move_error(const MoveArgs &a, int bit)
+{
+    if (a.error_word) atomicOr(a.error_word, bit);
+}
+
+// ---------------------------------------------------------------------------
+// Reordering of beams: beam j <- beam parent[j].  Lane j of each wave holds
+// parent[j]; the destinations of source s are one ballot.
+
+template <int WM>
+struct BeamMoves {
+    uint32_t to[WM];  // beams that take over beam s, itself aside
+};
+
+template <int WM>
+__device__ __forceinline__ BeamMoves<WM> beam_moves(const MoveArgs &a, int b)
+{
+    const int lane = threadIdx.x & 63;
+    int p = -1;
+    if (lane < a.W) p = a.parent[b * a.W + lane];
+    if (p >= a.W) {
+        move_error(a, SV_ERR_PARENT);
+        p = -1;
+    }
+    BeamMoves<WM> m;
+#pragma unroll
+    for (int s = 0; s < WM; ++s) m.to[s] = (uint32_t)__ballot(p == s && lane != s);
+    return m;
+}
+
+template <class T, int WM, int NV>
+__global__ __launch_bounds__(kBlock) void reorder_dense_kernel(const MoveArgs a)
+{
+    int blk = blockIdx.x;
+    const int chunk = blk % a.chunks;
+    blk /= a.chunks;
+    const int g = blk % a.G;
+    blk /= a.G;
+    const int b = blk % a.B, pool = blk / a.B;
+    int len = a.S;
+    if (a.length) {
+        len = a.length[b];
+        if (len < 0 || len > a.S) {
+            if (threadIdx.x == 0) move_error(a, SV_ERR_LENGTH);
+            return;
+        }
+    }
+    const int64_t n = (int64_t)len * a.row_vecs;
+    const int64_t v0 = (int64_t)chunk * (kBlock * NV);
+    if (v0 >= n) return;
+    const BeamMoves<WM> m = beam_moves<WM>(a, b);
+    const int64_t beam = (int64_t)a.G * a.S * a.row_vecs;  // vectors from beam to beam
+    T *base = reinterpret_cast<T *>(a.pool[pool]) + (int64_t)b * a.W * beam + (int64_t)g * a.S * a.row_vecs;
+    T x[WM][NV];
+#pragma unroll
+    for (int s = 0; s < WM; ++s)
+        if (m.to[s])
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int64_t v = v0 + i * kBlock + threadIdx.x;
+                if (v < n) x[s][i] = base[s * beam + v];
+            }
+#pragma unroll
+    for (int s = 0; s < WM; ++s)
+        for (uint32_t to = m.to[s]; to; to &= to - 1) {
+            const int j = __ffs(to) - 1;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int64_t v = v0 + i * kBlock + threadIdx.x;
+                if (v < n) base[j * beam + v] = x[s][i];
+            }
+        }
+}
+
+template <class T, int WM>
+__global__ __launch_bounds__(kBlock) void reorder_paged_kernel(const MoveArgs a)
+{
+    int blk = blockIdx.x;
+    const int chunk = blk % a.chunks;
+    blk /= a.chunks;
+    const int g = blk % a.G;
+    blk /= a.G;
+    const int b = blk % a.B, pool = blk / a.B;
+    int len = a.length[b];
+    const int from = a.start ? a.start[b] : 0;
+    const int most = a.max_blocks * a.S;
+    if (from < 0 || len < 0 || len > most || from > most) {
+        if (threadIdx.x == 0) move_error(a, SV_ERR_LENGTH);
+        return;
+    }
+    if (len > a.max_length) {
+        if (threadIdx.x == 0) move_error(a, SV_ERR_LENGTH);
+        len = a.max_length;
+    }
+    const int64_t v = (int64_t)chunk * kBlock + threadIdx.x;
+    const int64_t n = (int64_t)(len - from) * a.row_vecs;
+    if ((int64_t)chunk * kBlock >= n) return;
+    const BeamMoves<WM> m = beam_moves<WM>(a, b);  // every lane still here
+    if (v >= n) return;
+    const int r = (int)(v / a.row_vecs);
+    const int at = from + r, block = at / a.S;
+    const int64_t inside = ((int64_t)g * a.S + at % a.S) * a.row_vecs + (v - (int64_t)r * a.row_vecs);
+    const int64_t page_vecs = (int64_t)a.G * a.S * a.row_vecs;
+    const int32_t *table = a.table + (int64_t)b * a.W * a.max_blocks + block;
+    T *base = reinterpret_cast<T *>(a.pool[pool]) + inside;
+    int page[WM];
+    T x[WM];
+    bool bad = false;
+#pragma unroll
+    for (int s = 0; s < WM; ++s) page[s] = m.to[s] ? table[(int64_t)s * a.max_blocks] : -1;
+#pragma unroll
+    for (int s = 0; s < WM; ++s) {
+        if (!m.to[s]) continue;
+        if (page[s] < 0 || page[s] >= a.num_pages) {
+            bad = true;
+            page[s] = -1;
+        } else {
+            x[s] = base[page[s] * page_vecs];
+        }
+    }
+#pragma unroll
+    for (int s = 0; s < WM; ++s) {
+        if (page[s] < 0) continue;
+        for (uint32_t to = m.to[s]; to; to &= to - 1) {
+            const int p = table[(int64_t)(__ffs(to) - 1) * a.max_blocks];
+            if (p < 0 || p >= a.num_pages) bad = true;
+            else if (p != page[s]) base[p * page_vecs] = x[s];
+        }
+    }
+    if (bad) move_error(a, SV_ERR_PAGE);
+}
+
+// ---------------------------------------------------------------------------
+// The accepted path of a tree: row first + path[i] -> row first + i, i
+// ascending.  path[i] >= i, and a later source lies above every earlier
+// destination, so a thread that reads ahead of its writes reads what was
+// there before the call.
+
+constexpr int kPathAhead = 4;  // rows read before the first of them is written
+
+template <class T>
+__global__ __launch_bounds__(kBlock) void compact_kernel(const MoveArgs a)
+{
+    int blk = blockIdx.x;
+    const int chunk = blk % a.chunks;
+    blk /= a.chunks;
+    const int b = blk % a.B, pool = blk / a.B;
+    const int d = a.accepted[b];
+    if (d <= 0) return;
+    const int lane = threadIdx.x & 63;
+    const int32_t *path = a.path + (int64_t)b * a.N;
+    bool bad = d > a.N;
+    for (int i = lane; i < d && !bad; i += 64) {
+        const int p = path[i];
+        bad = p >= a.N || p <= (i ? path[i - 1] : -1);
+    }
+    if (__ballot(bad) != 0ull) {
+        if (threadIdx.x == 0) move_error(a, SV_ERR_TREE);
+        return;
+    }
+    const int len = a.length[b];
+    const int64_t base = (int64_t)len + a.first;
+    if (len < 0 || base + path[d - 1] >= (int64_t)a.max_blocks * a.S) {
+        if (threadIdx.x == 0) move_error(a, SV_ERR_LENGTH);
+        return;
+    }
+    const int v = chunk * kBlock + (int)threadIdx.x;
+    const int g = v / a.row_vecs;
+    if (g >= a.G) return;
+    const int32_t *table = a.table + (int64_t)b * a.max_blocks;
+    const int64_t page_vecs = (int64_t)a.G * a.S * a.row_vecs;
+    T *col = reinterpret_cast<T *>(a.pool[pool]) + (int64_t)g * a.S * a.row_vecs + (v - g * a.row_vecs);
+    for (int i0 = 0; i0 < d; i0 += kPathAhead) {
+        T x[kPathAhead];
+        T *to[kPathAhead];
+#pragma unroll
+        for (int k = 0; k < kPathAhead; ++k) {
+            to[k] = nullptr;
+            const int i = i0 + k;
+            if (i >= d || path[i] == i) continue;
+            const int from = (int)base + path[i], dest = (int)base + i;
+            const int pf = table[from / a.S], pd = table[dest / a.S];
+            if (pf < 0 || pf >= a.num_pages || pd < 0 || pd >= a.num_pages) {
+                if (threadIdx.x == 0) move_error(a, SV_ERR_PAGE);
+                continue;
+            }
+            to[k] = col + pd * page_vecs + (int64_t)(dest % a.S) * a.row_vecs;
+            x[k] = col[pf * page_vecs + (int64_t)(from % a.S) * a.row_vecs];
+        }
+#pragma unroll
+        for (int k = 0; k < kPathAhead; ++k)
+            if (to[k]) *to[k] = x[k];
+    }
+}
+
+// ---------------------------------------------------------------------------
+
+// Bytes per vector that every row of every pool allows.
+static int move_vector(void *const *pools, int32_t n, int64_t row_bytes)
+{
+    uintptr_t bits = (uintptr_t)row_bytes;
+    for (int32_t i = 0; i < n; ++i) bits |= (uintptr_t)pools[i];
+    return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 1;
+}
+
+static bool pools_ok(void *const *pools, int32_t n)
+{
+    if (n > 0 && !pools) return false;
+    for (int32_t i = 0; i < n; ++i)
+        if (!pools[i]) return false;
+    return true;
+}
+
+template <class T>
+static void launch_reorder(const MoveArgs &a, int n, hipStream_t s)
+{
+    const unsigned grid = (unsigned)((int64_t)n * a.B * a.G * a.chunks);
+    if (a.table) {
+        if (a.W <= 4) reorder_paged_kernel<T, 4><<<grid, kBlock, 0, s>>>(a);
+        else if (a.W <= 8) reorder_paged_kernel<T, 8><<<grid, kBlock, 0, s>>>(a);
+        else if (a.W <= 16) reorder_paged_kernel<T, 16><<<grid, kBlock, 0, s>>>(a);
+        else reorder_paged_kernel<T, 32><<<grid, kBlock, 0, s>>>(a);
+    } else {
+        if (a.W <= 4) reorder_dense_kernel<T, 4, 4><<<grid, kBlock, 0, s>>>(a);
+        else if (a.W <= 8) reorder_dense_kernel<T, 8, 2><<<grid, kBlock, 0, s>>>(a);
+        else if (a.W <= 16) reorder_dense_kernel<T, 16, 1><<<grid, kBlock, 0, s>>>(a);
+        else reorder_dense_kernel<T, 32, 1><<<grid, kBlock, 0, s>>>(a);
+    }
+}
+
+template <class T>
+static void launch_compact(const MoveArgs &a, int n, hipStream_t s)
+{
+    compact_kernel<T><<<(unsigned)((int64_t)n * a.B * a.chunks), kBlock, 0, s>>>(a);
+}
+
+// Chunks of the positions of one (pool, sequence, group), kBlock * NV vectors
+// each; 0 when the launch would be too large.
+static bool move_grid(MoveArgs &a, int32_t n_pools, int64_t vecs, int per_thread)
+{
+    const int64_t per = (int64_t)kBlock * per_thread;
+    const int64_t chunks = std::max<int64_t>(1, (vecs + per - 1) / per);
+    if (chunks >= ((int64_t)1 << 31) / std::min(n_pools, kMovePools) / a.B / a.G) return false;
+    a.chunks = (int32_t)chunks;
+    return true;
+}
+
+enum Move { kReorder, kCompact };
+
+static int32_t move_launch(MoveArgs &a, Move what, void *const *pools, int32_t n_pools, int64_t row_bytes,
+                           int64_t positions, hipStream_t s)
+{
+    const int vb = move_vector(pools, n_pools, row_bytes);
+    if (row_bytes / vb >= ((int64_t)1 << 31)) return SV_EINVAL;
+    a.row_vecs = (int32_t)(row_bytes / vb);
+    const int nv = what == kReorder && !a.table ? (a.W <= 4 ? 4 : a.W <= 8 ? 2 : 1) : 1;
+    if (what == kCompact) {
+        // a thread's column is a vector of one of the G rows of a position
+        if ((int64_t)a.G * a.row_vecs >= ((int64_t)1 << 31) - kBlock) return SV_EINVAL;
+        const int32_t G = a.G;
+        a.G = 1;
+        const bool ok = move_grid(a, n_pools, (int64_t)G * a.row_vecs, 1);
+        a.G = G;
+        if (!ok) return SV_EINVAL;
+    } else if (!move_grid(a, n_pools, positions * a.row_vecs, nv)) {
+        return SV_EINVAL;
+    }
+    for (int32_t p0 = 0; p0 < n_pools; p0 += kMovePools) {
+        const int n = std::min(kMovePools, n_pools - p0);
+        for (int i = 0; i < n; ++i) a.pool[i] = static_cast<char *>(pools[p0 + i]);
+        if (what == kReorder) {
+            if (vb == 16) launch_reorder<u32x4>(a, n, s);
+            else if (vb == 4) launch_reorder<uint32_t>(a, n, s);
+            else launch_reorder<uint8_t>(a, n, s);
+        } else {
+            if (vb == 16) launch_compact<u32x4>(a, n, s);
+            else if (vb == 4) launch_compact<uint32_t>(a, n, s);
+            else launch_compact<uint8_t>(a, n, s);
+        }
+    }
+    return hipGetLastError() == hipSuccess ? SV_OK : SV_EHIP;
+}
+
+static bool paged_ok(int32_t G, int32_t page_size, int64_t row_bytes, int32_t num_pages, int32_t max_blocks)
+{
+    return G >= 1 && page_size >= 1 && row_bytes >= 1 && num_pages >= 0 && max_blocks >= 1 &&
+           (int64_t)max_blocks * page_size < ((int64_t)1 << 31) && row_bytes < ((int64_t)1 << 31) &&
+           (double)num_pages * G * page_size * (double)row_bytes < 0x1p62;
+}
+
+}  // namespace sv
+
+extern "C" {
+
+int32_t spec_beam_reorder(void *const *pools, int32_t n_pools, int32_t B, int32_t W, int32_t G, int32_t S,
+                          int64_t row_bytes, const int32_t *parent, const int32_t *length, int32_t *error_word,
+                          void *stream)
+{
+    if (n_pools < 0 || n_pools > SV_MAX_POOLS || B < 0 || W < 1 || W > SV_MAX_BEAMS || G < 1 || S < 0 ||
+        row_bytes < 1 || row_bytes >= ((int64_t)1 << 31) ||
+        (double)B * W * G * S * (double)row_bytes >= 0x1p62)
+        return SV_EINVAL;
+    if (B == 0 || n_pools == 0 || S == 0) return SV_OK;
+    if (!sv::pools_ok(pools, n_pools) || !parent) return SV_EINVAL;
+    sv::MoveArgs a = {};
+    a.parent = parent;
+    a.length = length;
+    a.error_word = error_word;
+    a.B = B;
+    a.W = W;
+    a.G = G;
+    a.S = S;
+    return sv::move_launch(a, sv::kReorder, pools, n_pools, row_bytes, S, static_cast<hipStream_t>(stream));
+}
+
+int32_t spec_beam_reorder_paged(void *const *pools, int32_t n_pools, int32_t B, int32_t W, int32_t G,
+                                int32_t page_size, int64_t row_bytes, int32_t num_pages,
+                                const int32_t *block_table, int32_t max_blocks, const int32_t *parent,
+                                const int32_t *start, const int32_t *length, int32_t max_length,
+                                int32_t *error_word, void *stream)
+{
+    if (n_pools < 0 || n_pools > SV_MAX_POOLS || B < 0 || W < 1 || W > SV_MAX_BEAMS || max_length < 0 ||
+        !sv::paged_ok(G, page_size, row_bytes, num_pages, max_blocks) ||
+        (int64_t)max_length > (int64_t)max_blocks * page_size)
+        return SV_EINVAL;
+    if (B == 0 || n_pools == 0 || max_length == 0) return SV_OK;
+    if (!sv::pools_ok(pools, n_pools) || !parent || !length || !block_table) return SV_EINVAL;
+    sv::MoveArgs a = {};
+    a.table = block_table;
+    a.parent = parent;
+    a.start = start;
+    a.length = length;
+    a.error_word = error_word;
+    a.B = B;
+    a.W = W;
+    a.G = G;
+    a.S = page_size;
+    a.num_pages = num_pages;
+    a.max_blocks = max_blocks;
+    a.max_length = max_length;
+    return sv::move_launch(a, sv::kReorder, pools, n_pools, row_bytes, max_length,
+                           static_cast<hipStream_t>(stream));
+}
+
+int32_t spec_cache_compact(void *const *pools, int32_t n_pools, int32_t B, int32_t G, int32_t page_size,
+                           int64_t row_bytes, int32_t num_pages, const int32_t *block_table, int32_t max_blocks,
+                           const int32_t *seq_len, int32_t first, const int32_t *path,
+                           const int32_t *accepted_len, int32_t N, int32_t *error_word, void *stream)
+{
+    if (n_pools < 0 || n_pools > SV_MAX_POOLS || B < 0 || N < 0 || N > 128 || first < 0 ||
+        !sv::paged_ok(G, page_size, row_bytes, num_pages, max_blocks))
+        return SV_EINVAL;
+    if (B == 0 || n_pools == 0 || N == 0) return SV_OK;
+    if (!sv::pools_ok(pools, n_pools) || !block_table || !seq_len || !path || !accepted_len) return SV_EINVAL;
+    sv::MoveArgs a = {};
+    a.table = block_table;
+    a.length = seq_len;
+    a.first = first;
+    a.path = path;
+    a.accepted = accepted_len;
+    a.N = N;
+    a.error_word = error_word;
+    a.B = B;
+    a.W = 1;
+    a.G = G;
+    a.S = page_size;
+    a.num_pages = num_pages;
+    a.max_blocks = max_blocks;
+    return sv::move_launch(a, sv::kCompact, pools, n_pools, row_bytes, 1, static_cast<hipStream_t>(stream));
+}
+
+}  // extern "C"
