@@ -2,25 +2,24 @@
 //
 //   c(w, v) = s_w + z_w(v) / T - ln sum_u exp(z_w(u) / T)
 //
-// Within a beam c rises with z, so a beam's best M candidates are its M
-// largest logits, and the best M of a sequence are among the W beams' lists:
 //   1. beam_rows_kernel   one workgroup per (row, chunk): one pass over the
-//                         logits for the running maximum and the sum of
-//                         exponentials, and the chunk's M largest logits.
-//   2. beam_merge_kernel  one workgroup per sequence: the rows' normalisers,
-//                         c in fp64 for W * chunks * M candidates, the best M.
+//                         logits for the maximum and the sum of exponentials.
+//   2. beam_merge_kernel  one workgroup per sequence: the rows' normalisers
+//                         and the best M candidates.
 //
 // The pass is bound by reading the logits, and on bf16 nearly by its
-// exponentials (eight per 16 bytes), so it may not spend VALU on keeping
-// lists.  While it streams it keeps only maxima: of each lane over the chunk
-// and of each lane over groups of tiles (LDS, at most kGroups a lane).  The
-// M-th largest of the 256 lanes' maxima is a floor under the chunk's M-th
-// largest logit, since M lanes hold one at least as large each.  Few logits
-// reach it (M ln-like: the best k fall on 256 lanes at random, so ~M (1 +
-// M/512)), and they lie in the groups whose maximum does, which their lanes
-// read again; the survivors are ranked by counting.
+// exponentials (eight per 16 bytes), so it keeps no lists: beside the sums it
+// leaves only the maxima of `cols` columns of its chunk (column l: vectors l,
+// l + cols, ...), which its lanes hold anyway.  c rises with z within a beam,
+// so the merge turns the maxima into c and takes the M-th largest over all
+// columns of the sequence as a floor: M columns hold a candidate at least as
+// large each, so no smaller one is among the best M.  Only the columns whose
+// maximum reaches the floor, about M, are read again, all at once; what
+// reaches the floor there is ranked by counting.  A sequence has between 1024
+// and 2048 columns (fewer for short rows): the merge holds eight a thread, and
+// more columns leave less to read again.
 #include <algorithm>
-#include <climits>
+#include <cfloat>
 
 #include "specdecode.h"
 #include "sv_internal.h"
@@ -30,14 +29,18 @@
 
 namespace sv {
 
+constexpr double kLn2 = 0.6931471805599453;
 constexpr int kBeamLoads = 4;        // 16-byte vectors per thread per tile
-constexpr int kBeamGroups = 16;      // groups of tiles per lane with a maximum of their own
 constexpr int kBeamFill = 768;       // workgroups the streaming grid aims for
-constexpr int kBeamMaxChunks = 64;   // chunks per row: one per lane when the merge reads them
-constexpr int kBeamLists = 8192;     // W * chunks * M at most: the merge's candidates per sequence
-constexpr int kBeamKeep = 512;       // survivors ranked at once
-constexpr int kBeamRound = kBlock * 8;  // most survivors of one vector per thread
-constexpr int kBeamSlow = kBeamRound + SV_MAX_CANDIDATES;
+constexpr int kBeamMaxChunks = 64;   // chunks per row: the merge gives each a lane
+constexpr int kBeamRowChunks = 256;  // W * chunks at most: with lanes to spare, one thread each in the merge
+constexpr int kBeamPre = 8;          // column maxima per thread of the merge
+constexpr int kMerge = 1024;         // threads of the merge: 256 hold columns, all of them read columns again
+constexpr int kBeamAgain = 2;        // vectors each requests at once
+constexpr int kBeamHits = 256;       // columns read again
+constexpr int kBeamKeep = 512;       // candidates ranked at once
+constexpr int kBeamRound = 256;      // vectors the slow path takes at once
+constexpr int kBeamSlow = kBeamRound * 8 + SV_MAX_CANDIDATES;  // their keys and the best so far
 
 struct BeamPart {
     float m;     // chunk maximum
@@ -50,16 +53,17 @@ struct BeamArgs {
     const float *scores, *temperature;
     const int32_t *finished;
     int64_t seq_bytes, beam_bytes;
-    int32_t B, W, V, M, eos, nvec, nc, cvec, gt;  // gt: tiles per group
+    int32_t B, W, V, M, eos, nvec, nc, cvec, cols_log, aligned;
+    int32_t per, g_log;  // the merge: columns per thread, 1 << g_log >= nc lanes per row
     BeamPart *part;     // [B][W][nc]
-    uint64_t *keys;     // [B][W][nc][M] descending, 0 = none
+    float *cols;        // [B][W][nc][1 << cols_log] column maxima
     float *out_score;
     int32_t *out_parent, *out_token, *out_finished, *error_word;
 };
 
 struct BeamPlan {
-    int32_t nvec, nc, cvec, gt;
-    size_t off_keys, bytes;
+    int32_t nvec, nc, cvec, cols_log, per, g_log;
+    size_t off_cols, bytes;
 };
 
 static bool make_beam_plan(int32_t B, int32_t W, int32_t V, int32_t dtype, int32_t M, BeamPlan *p)
@@ -72,15 +76,19 @@ static bool make_beam_plan(int32_t B, int32_t W, int32_t V, int32_t dtype, int32
     const int64_t rows = (int64_t)std::max(B, 1) * W;
     int64_t nc = (kBeamFill + rows - 1) / rows;
     nc = std::min<int64_t>(nc, std::max(1, p->nvec / kBlock));
-    nc = std::min<int64_t>(nc, std::min(kBeamMaxChunks, std::max(1, kBeamLists / (W * M))));
+    nc = std::min<int64_t>(nc, std::min(kBeamMaxChunks, std::max(1, kBeamRowChunks / W)));
     p->cvec = (int32_t)((p->nvec + nc - 1) / nc);
     p->nc = (p->nvec + p->cvec - 1) / p->cvec;
-    const int32_t tiles = (p->cvec + kBlock * kBeamLoads - 1) / (kBlock * kBeamLoads);
-    p->gt = (tiles + kBeamGroups - 1) / kBeamGroups;
-    if (rows * p->nc * M >= ((int64_t)1 << 31)) return false;
+    p->cols_log = 8;  // W * nc <= 256, so at least 8 columns
+    while (((int64_t)W * p->nc) << p->cols_log > kBeamPre * kBlock) --p->cols_log;
+    if ((rows * p->nc) << p->cols_log >= ((int64_t)1 << 31)) return false;
+    p->per = 1;
+    while (p->per * kBlock < (W * p->nc) << p->cols_log) p->per <<= 1;
+    p->g_log = 0;
+    while (1 << p->g_log < p->nc) ++p->g_log;
     auto align = [](size_t x) { return (x + 255) & ~(size_t)255; };
-    p->off_keys = align(sizeof(BeamPart) * (size_t)(rows * p->nc));
-    p->bytes = align(p->off_keys + sizeof(uint64_t) * (size_t)(rows * p->nc * M));
+    p->off_cols = align(sizeof(BeamPart) * (size_t)(rows * p->nc));
+    p->bytes = align(p->off_cols + sizeof(float) * (size_t)((rows * p->nc) << p->cols_log));
     return true;
 }
 
@@ -100,6 +108,12 @@ __device__ __forceinline__ bool beam_wide(float m, const ExpScale &e)
 __device__ __forceinline__ double beam_offset(float m, const ExpScale &e)
 {
     return beam_wide(m, e) ? (double)m * e.c64 : (double)(m * e.c);
+}
+
+// A sum taken against the offset of m, against that of M >= m.
+__device__ __forceinline__ double beam_rebase(double s, float m, float M, const ExpScale &e)
+{
+    return m == -INFINITY ? s : s * exp2(beam_offset(m, e) - beam_offset(M, e));
 }
 
 struct BeamRun {
@@ -155,158 +169,51 @@ __device__ __forceinline__ float beam_tile(const uint4 (&r)[U], const ExpScale &
     return lm;
 }
 
-// ---------------------------------------------------------------------------
-// The chunk's M largest logits when more than kBeamKeep reach the floor (many
-// equal ones): vectors in index order, one per thread a round, those that
-// beat the best M so far collected and cut back to M.  Ends early when the
-// M-th best equals the chunk's maximum: whatever follows has a larger index.
-
-// The best M of buf[0, n), n >= M, moved to its front (unordered): the M-th
-// largest key by its bits from the top, counting.
-__device__ __forceinline__ uint64_t beam_cut(uint64_t *buf, int n, int M, int *cnt, int *ldsi)
-{
-    uint64_t kth = 0;
-    for (int bit = 63; bit >= 0; --bit) {
-        const uint64_t c = kth | (1ull << bit);
-        int k = 0;
-        for (int i = threadIdx.x; i < n; i += kBlock) k += buf[i] >= c;
-        k = wave_sum_int(k);
-        if ((threadIdx.x & 63) == 0) ldsi[threadIdx.x >> 6] = k;
-        __syncthreads();
-        k = ldsi[0] + ldsi[1] + ldsi[2] + ldsi[3];
-        __syncthreads();
-        if (k >= M) kth = c;
-    }
-    // keys are distinct: M of them are >= kth
-    constexpr int kOwn = (kBeamSlow + kBlock - 1) / kBlock;
-    uint64_t own[kOwn];
-#pragma unroll
-    for (int j = 0; j < kOwn; ++j) {
-        const int i = threadIdx.x + j * kBlock;
-        own[j] = i < n ? buf[i] : 0;
-    }
-    if (threadIdx.x == 0) *cnt = 0;
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kOwn; ++j)
-        if (own[j] >= kth) buf[atomicAdd(cnt, 1)] = own[j];
-    __syncthreads();
-    return kth;
-}
-
-template <int DT, bool ALIGNED>
-__device__ __noinline__ int beam_collect_slow(const char *row, int q0, int q1, int V, float tau, float top, int M,
-                                              uint64_t *buf, int *cnt, int *ldsi)
-{
-    constexpr int VEC = Elt<DT>::kVec;
-    uint64_t floor = 0;
-    if (threadIdx.x == 0) *cnt = 0;
-    __syncthreads();
-    int n = 0;
-    for (int qb = q0; qb < q1; qb += kBlock) {
-        PairTileU<1> r;
-        issue_pair<DT, ALIGNED, false>(row, nullptr, qb, q1, V, r);
-        fix_pair<DT, false>(qb, q1, V, r);
-        float x[VEC];
-        Elt<DT>::unpack(r.t[0], x);
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-            const uint64_t key = top_key(x[k], elem_index(qb, 0, k, VEC));
-            if (x[k] >= tau && x[k] > -INFINITY && key > floor) buf[atomicAdd(cnt, 1)] = key;
-        }
-        __syncthreads();
-        n = *cnt;
-        __syncthreads();
-        if (n > SV_MAX_CANDIDATES) {
-            floor = beam_cut(buf, n, M, cnt, ldsi);
-            n = M;
-            if (key_value(floor) == top) break;
-        }
-    }
-    return n;
-}
-
 template <int DT, bool ALIGNED>
 __device__ __forceinline__ void beam_chunk(const BeamArgs &a, const char *row, int slot, int chunk, float T)
 {
-    constexpr int VEC = Elt<DT>::kVec;
-    constexpr int U = kBeamLoads, kStep = kBlock * kBeamLoads;
-    __shared__ __align__(16) char lds[kBeamGroups * kBlock * 4 + kBeamKeep * 8];
-    static_assert(sizeof(lds) >= kBeamSlow * 8, "the slow path's buffer");
-    __shared__ float lds_k[kBlock + 1];
-    __shared__ double lds_d[kWaves];
-    __shared__ int lds_i[kWaves], cnt;
-    float *gm = reinterpret_cast<float *>(lds);
-    uint64_t *buf = reinterpret_cast<uint64_t *>(lds + kBeamGroups * kBlock * 4);
-    const int tid = threadIdx.x;
+    constexpr int U = kBeamLoads;
+    __shared__ float lds_col[kBlock], lds_m[kWaves];
+    __shared__ double lds_s[kWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int q0 = chunk * a.cvec, q1 = min(a.nvec, q0 + a.cvec);
     PairTileU<U> ra;
     issue_pair<DT, ALIGNED, false>(row, nullptr, q0, q1, a.V, ra);
     const ExpScale e = make_scale(T);
     BeamRun run = {-INFINITY, -INFINITY, false, 0.0};
-    float best = -INFINITY, gmax = -INFINITY;
-    int t = 0, g = 0;
+    float best = -INFINITY;
     stream_pair<DT, ALIGNED, false>(row, nullptr, q0, q1, a.V, ra, [&](const PairTileU<U> &r, int) {
-        const float lm = beam_tile<DT, U>(r.t, e, run);
-        best = fmaxf(best, lm);
-        gmax = fmaxf(gmax, lm);
-        if (++t == a.gt) {
-            gm[g * kBlock + tid] = gmax;
-            gmax = -INFINITY;
-            t = 0;
-            ++g;
-        }
+        best = fmaxf(best, beam_tile<DT, U>(r.t, e, run));
     });
-    if (t) gm[g++ * kBlock + tid] = gmax;
-    // normaliser of the chunk
-    const float top = block_max(run.m, lds_k);
-    const double sc = run.m == -INFINITY ? run.s : run.s * exp2(beam_offset(run.m, e) - beam_offset(top, e));
-    const double sum = block_sum(sc, lds_d);
-    if (tid == 0) {
-        a.part[(size_t)slot * a.nc + chunk] = {top, 0, sum};
-        cnt = 0;
-    }
-    // candidates
-    const float tau = block_kth(best, a.M, lds_k);
-    if (best >= tau && best > -INFINITY) {
-        for (int h = 0; h < g; ++h) {
-            if (!(gm[h * kBlock + tid] >= tau)) continue;
-            for (int i = 0; i < a.gt; ++i) {
-                const int qb = q0 + (h * a.gt + i) * kStep;
-                if (qb >= q1) break;
-                PairTileU<U> r;
-                issue_pair<DT, ALIGNED, false>(row, nullptr, qb, q1, a.V, r);
-                fix_pair<DT, false>(qb, q1, a.V, r);
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    float x[VEC];
-                    Elt<DT>::unpack(r.t[u], x);
-#pragma unroll
-                    for (int k = 0; k < VEC; ++k)
-                        if (x[k] >= tau && x[k] > -INFINITY) {
-                            const int at = atomicAdd(&cnt, 1);
-                            if (at < kBeamKeep) buf[at] = top_key(x[k], elem_index(qb, u, k, VEC));
-                        }
-                }
-            }
-        }
+    const double s = wave_sum(run.s);  // against the wave's maximum
+    // column l of C: threads l, l + C, ...
+    const int C = 1 << a.cols_log;
+    if (C < 64) best = fmaxf(best, lane_xor<32>(best));
+    if (C < 32) best = fmaxf(best, lane_xor<16>(best));
+    if (C < 16) best = fmaxf(best, lane_xor<8>(best));
+    lds_col[threadIdx.x] = best;
+    if (lane == 0) {
+        lds_m[wave] = run.m;
+        lds_s[wave] = s;
     }
     __syncthreads();
-    int n = cnt;
-    if (n > kBeamKeep) {
-        __syncthreads();
-        buf = reinterpret_cast<uint64_t *>(lds);
-        n = beam_collect_slow<DT, ALIGNED>(row, q0, q1, a.V, tau, top, a.M, buf, &cnt, lds_i);
+    const size_t at = (size_t)slot * a.nc + chunk;
+    if ((int)threadIdx.x < C) {
+        for (int i = max(C, 64); i < kBlock; i += max(C, 64)) best = fmaxf(best, lds_col[threadIdx.x + i]);
+        a.cols[(at << a.cols_log) + threadIdx.x] = best;
     }
-    // distinct keys: a key's place is the number of larger ones
-    uint64_t *out = a.keys + ((size_t)slot * a.nc + chunk) * a.M;
-    for (int i = tid; i < n; i += kBlock) {
-        const uint64_t k = buf[i];
-        int rank = 0;
-        for (int j = 0; j < n; ++j) rank += buf[j] > k;
-        if (rank < a.M) out[rank] = k;
-    }
-    for (int i = n + tid; i < a.M; i += kBlock) out[i] = 0;
+    if (wave != 0) return;
+    const float top = fmaxf(fmaxf(lds_m[0], lds_m[1]), fmaxf(lds_m[2], lds_m[3]));
+    double sum = 0.0;
+    if (lane < kWaves) sum = beam_rebase(lds_s[lane], lds_m[lane], top, e);
+    sum += dpp_double<kDppQuadXor1>(sum);
+    sum += dpp_double<kDppQuadXor2>(sum);
+    if (lane == 0) a.part[at] = {top, 0, sum};
+}
+
+__device__ __forceinline__ const char *beam_row(const BeamArgs &a, int b, int w)
+{
+    return a.logits + b * a.seq_bytes + w * a.beam_bytes;
 }
 
 __device__ __forceinline__ bool beam_temperature_ok(float T) { return T > 0.f && T < INFINITY; }
@@ -325,7 +232,7 @@ __global__ __launch_bounds__(kBlock) void beam_rows_kernel(const BeamArgs a)
     const int b = slot / a.W, w = slot % a.W;
     const float T = a.temperature ? a.temperature[b] : 1.f;
     if (!beam_temperature_ok(T) || !beam_live(a, slot)) return;
-    beam_chunk<DT, ALIGNED>(a, a.logits + b * a.seq_bytes + w * a.beam_bytes, slot, chunk, T);
+    beam_chunk<DT, ALIGNED>(a, beam_row(a, b, w), slot, chunk, T);
 }
 
 // ---------------------------------------------------------------------------
@@ -354,73 +261,244 @@ __device__ __forceinline__ bool ahead(const BeamCand &x, const BeamCand &y)
     return x.c > y.c || (x.c == y.c && (x.w < y.w || (x.w == y.w && x.key > y.key)));
 }
 
-struct BeamRows {
-    double base[SV_MAX_BEAMS];  // s_w - ln sum_u exp((z(u) - m) / T)
-    float m[SV_MAX_BEAMS];
-    int state[SV_MAX_BEAMS];    // 0: no candidate, 1: its row's, 2: finished
+struct __align__(16) BeamRow {
+    double base;  // s_w - ln sum_u exp((z(u) - m) / T)
+    float m;
+    int state;    // 0: no candidate, 1: its row's, 2: finished
 };
 
-__device__ __forceinline__ BeamCand beam_candidate(const BeamArgs &a, const BeamRows &r, const uint64_t *keys,
-                                                   int i, double inv_t)
+// c of logit x of a row in the running.
+__device__ __forceinline__ double beam_c(const BeamRow &r, float x, double inv_t)
 {
-    const int per = a.nc * a.M, w = i / per;
-    BeamCand c = {0, 0, w};
-    if (r.state[w] == 1) {
-        c.key = keys[i];
-        if (c.key) c.c = double_order(r.base[w] + ((double)key_value(c.key) - (double)r.m[w]) * inv_t);
-    } else if (r.state[w] == 2 && i == w * per) {
-        c.key = top_key(0.f, a.eos);
-        c.c = double_order(r.base[w]);
-    }
-    return c;
+    return r.base + ((double)x - (double)r.m) * inv_t;
 }
 
-__global__ __launch_bounds__(kBlock) void beam_merge_kernel(const BeamArgs a)
+// c rounded to fp32 for floors, where order may be lost but not reversed, and
+// held above -inf, which stands for no candidate.
+__device__ __forceinline__ float beam_rough(double c) { return fmaxf((float)c, -FLT_MAX); }
+
+// Sum and maximum over aligned groups of G lanes (a power of two up to 64).
+template <class T, class Op>
+__device__ __forceinline__ T group_reduce(T v, int G, Op op)
 {
-    __shared__ BeamRows rows;
-    __shared__ BeamCand cand[kBeamKeep];
-    __shared__ uint64_t lds_k[kBlock + 1];
-    __shared__ int cnt, errors;
-    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    if (tid == 0) {
-        cnt = 0;
-        errors = 0;
+    if (G > 1) v = op(v, lane_xor<1>(v));
+    if (G > 2) v = op(v, lane_xor<2>(v));
+    if (G > 4) v = op(v, lane_xor<4>(v));
+    if (G > 8) v = op(v, lane_xor<8>(v));
+    if (G > 16) v = op(v, lane_xor<16>(v));
+    if (G > 32) v = op(v, lane_xor<32>(v));
+    return v;
+}
+
+// Vector q of a row with elements at or beyond V as -inf (for the slow path).
+template <int DT>
+__device__ __forceinline__ uint4 beam_vector(const BeamArgs &a, const char *row, int q)
+{
+    constexpr int VEC = Elt<DT>::kVec;
+    const char *p = row + (size_t)q * 16;
+    const int valid = min(VEC, a.V - q * VEC);
+    uint4 r;
+    if (a.aligned) r = *reinterpret_cast<const uint4 *>(p);
+    else r = load16_unaligned(p, ((uint32_t)((uintptr_t)p & 15)) + (uint32_t)valid * Elt<DT>::kBytes > 16u);
+    if (valid < VEC) mask_raw<DT>(r, valid);
+    return r;
+}
+
+// ---------------------------------------------------------------------------
+// When more candidates reach the floor than are ranked at once (many equal
+// ones), row by row: the best M keys of a row, vectors in index order, kBeamRound
+// at a time, those that beat the best M so far collected and cut back to
+// M.  A row ends early when its M-th best logit equals its maximum: whatever
+// follows has a larger index.
+
+// The best M of buf[0, n), n >= M, moved to its front (unordered): the M-th
+// largest key by its bits from the top, counting.
+__device__ __forceinline__ uint64_t beam_cut(uint64_t *buf, int n, int M, int *cnt, int *ldsi)
+{
+    uint64_t kth = 0;
+    for (int bit = 63; bit >= 0; --bit) {
+        const uint64_t c = kth | (1ull << bit);
+        int k = 0;
+        for (int i = threadIdx.x; i < n; i += kMerge) k += buf[i] >= c;
+        k = wave_sum_int(k);
+        if ((threadIdx.x & 63) == 0) ldsi[threadIdx.x >> 6] = k;
+        __syncthreads();
+        k = 0;
+        for (int i = 0; i < kMerge / 64; ++i) k += ldsi[i];
+        __syncthreads();
+        if (k >= M) kth = c;
     }
+    // keys are distinct: M of them are >= kth
+    constexpr int kOwn = (kBeamSlow + kMerge - 1) / kMerge;
+    uint64_t own[kOwn];
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+        const int i = threadIdx.x + j * kMerge;
+        own[j] = i < n ? buf[i] : 0;
+    }
+    if (threadIdx.x == 0) *cnt = 0;
     __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j)
+        if (own[j] >= kth) buf[atomicAdd(cnt, 1)] = own[j];
+    __syncthreads();
+    return kth;
+}
+
+template <int DT>
+__device__ __forceinline__ int beam_row_slow(const BeamArgs &a, const BeamRow &r, const char *row, float floor_c,
+                                          double inv_t, uint64_t *buf, int *cnt, int *ldsi)
+{
+    constexpr int VEC = Elt<DT>::kVec;
+    uint64_t floor = 0;
+    if (threadIdx.x == 0) *cnt = 0;
+    __syncthreads();
+    int n = 0;
+    for (int qb = 0; qb < a.nvec; qb += kBeamRound) {
+        const int q = qb + (int)threadIdx.x;
+        if ((int)threadIdx.x < kBeamRound && q < a.nvec) {
+            float x[VEC];
+            Elt<DT>::unpack(beam_vector<DT>(a, row, q), x);
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                if (!(x[k] > -INFINITY) || beam_rough(beam_c(r, x[k], inv_t)) < floor_c) continue;
+                const uint64_t key = top_key(x[k], q * VEC + k);
+                if (key > floor) buf[atomicAdd(cnt, 1)] = key;
+            }
+        }
+        __syncthreads();
+        n = *cnt;
+        __syncthreads();
+        if (n > SV_MAX_CANDIDATES) {
+            floor = beam_cut(buf, n, a.M, cnt, ldsi);
+            n = a.M;
+            if (key_value(floor) == r.m) break;
+        }
+    }
+    return n;
+}
+
+// The best M into cand[0, n) in order; returns n.
+template <int DT>
+__device__ __forceinline__ int beam_slow(const BeamArgs &a, const BeamRow *rows, int b, float floor_c, double inv_t,
+                                      BeamCand *cand, uint64_t *buf, int *cnt, int *ldsi)
+{
+    int n = 0;
+    for (int w = 0; w < a.W; ++w) {
+        const BeamRow r = rows[w];
+        if (r.state == 0) continue;
+        const double top = r.base;  // of its best, c at z = m
+        if (n == a.M && double_order(top) <= cand[n - 1].c) continue;  // a later beam loses a tie
+        int k = 1;
+        if (r.state == 1) k = beam_row_slow<DT>(a, r, beam_row(a, b, w), floor_c, inv_t, buf, cnt, ldsi);
+        __syncthreads();
+        for (int i = threadIdx.x; i < k; i += kMerge) {
+            const uint64_t key = r.state == 2 ? top_key(0.f, a.eos) : buf[i];
+            const double c = r.state == 2 ? r.base : beam_c(r, key_value(key), inv_t);
+            cand[n + i] = {double_order(c), key, w};
+        }
+        __syncthreads();
+        BeamCand own = {0, 0, 0};
+        int rank = a.M;
+        if ((int)threadIdx.x < n + k) {
+            own = cand[threadIdx.x];
+            rank = 0;
+            for (int j = 0; j < n + k; ++j) rank += ahead(cand[j], own);
+        }
+        __syncthreads();
+        if (rank < a.M) cand[rank] = own;
+        n = min(n + k, a.M);
+        __syncthreads();
+    }
+    return n;
+}
+static_assert(2 * SV_MAX_CANDIDATES <= kMerge, "a row's best beside the best so far, one per thread");
+
+// A 16-byte vector requested now and put together later: of an unaligned
+// address the two aligned blocks that hold its `valid` elements (the first
+// one twice where it holds them all).
+template <int DT, bool ALIGNED>
+struct BeamLoad {
+    u32x4 x, y;
+    uint32_t sh;
+    __device__ __forceinline__ void issue(const char *p, int valid)
+    {
+        sh = ALIGNED ? 0u : (uint32_t)((uintptr_t)p & 15);
+        const u32x4 *blk = reinterpret_cast<const u32x4 *>(p - sh);
+        x = blk[0];
+        if (!ALIGNED) y = blk[sh + (uint32_t)valid * Elt<DT>::kBytes > 16u ? 1 : 0];
+    }
+    __device__ __forceinline__ uint4 vector() const
+    {
+        if (ALIGNED) return make_uint4(x.x, x.y, x.z, x.w);
+        // words sh / 4 + 0..4 of the eight
+        const bool one = sh & 4u, two = sh & 8u;
+        const uint32_t a0 = one ? x.y : x.x, a1 = one ? x.z : x.y, a2 = one ? x.w : x.z, a3 = one ? y.x : x.w;
+        const uint32_t a4 = one ? y.y : y.x, a5 = one ? y.z : y.y, a6 = one ? y.w : y.z;
+        const uint32_t f0 = two ? a2 : a0, f1 = two ? a3 : a1, f2 = two ? a4 : a2, f3 = two ? a5 : a3;
+        const uint32_t f4 = two ? a6 : a4, r = sh & 3u;
+        return make_uint4(funnel_bytes(f0, f1, r), funnel_bytes(f1, f2, r), funnel_bytes(f2, f3, r),
+                          funnel_bytes(f3, f4, r));
+    }
+};
+
+static_assert(2 * kBeamRowChunks <= kMerge, "a thread for each chunk of a sequence, a power of two a row");
+
+template <int DT, bool ALIGNED>
+__global__ __launch_bounds__(kMerge) void beam_merge_kernel(const BeamArgs a)
+{
+    __shared__ BeamRow rows[SV_MAX_BEAMS];
+    __shared__ float low[SV_MAX_BEAMS];  // no smaller logit of the row reaches the floor
+    __shared__ __align__(16) char lds[kBeamSlow * 8];
+    __shared__ BeamCand cand[kBeamKeep];
+    __shared__ int hits[kBeamHits];
+    __shared__ float lds_k[kBlock + 1];
+    __shared__ int n_hits, n_cand, errors, lds_i[kMerge / 64];
+    const int b = blockIdx.x, tid = threadIdx.x;
+    const int n_cols = (a.W * a.nc) << a.cols_log;
+    // everything the normalisers and the floor need is requested at once: a
+    // barrier waits for the loads before it
+    const float *cols = a.cols + (size_t)b * n_cols;
+    // (this thread's columns follow each other, so they are one row's)
+    const int per = a.per;
+    const int col0 = min(tid * per, n_cols - per);
+    const bool mine = tid < kBlock && tid * per < n_cols;
+    float x[kBeamPre];
+#pragma unroll
+    for (int j = 0; j < kBeamPre; ++j) x[j] = cols[col0 + min(j, per - 1)];
+    // G lanes to a row, one per chunk; W G <= 2 W nc, so each thread has one
+    const int G = 1 << a.g_log;
+    const int w = min(tid >> a.g_log, a.W - 1), chunk = tid & (G - 1), slot = b * a.W + w;
+    const float s = a.scores[slot];
+    BeamPart p = a.part[(size_t)slot * a.nc + min(chunk, a.nc - 1)];
+    const bool ended = a.finished && a.finished[slot];
     const float T = a.temperature ? a.temperature[b] : 1.f;
+    if (tid == 0) n_hits = n_cand = errors = 0;
+    __syncthreads();
     const bool good_t = beam_temperature_ok(T);
-    if (!good_t && tid == 0) errors = SV_ERR_TEMPERATURE;
     const ExpScale e = make_scale(good_t ? T : 1.f);
-    for (int w = wave; w < a.W && good_t; w += kWaves) {
-        const int slot = b * a.W + w;
-        const float s = a.scores[slot];
-        const bool ended = a.finished && a.finished[slot];
-        int state = 0;
+    if (!good_t && tid == 0) errors = SV_ERR_TEMPERATURE;
+    if (chunk >= a.nc) p = {-INFINITY, 0, 0.0};
+    const float m = group_reduce(p.m, G, [](float u, float v) { return fmaxf(u, v); });
+    const double sum = group_reduce(beam_rebase(p.s, p.m, m, e), G, [](double u, double v) { return u + v; });
+    if (chunk == 0 && tid < a.W * G) {
+        int state = 0, bad = 0;
         double base = (double)s;
-        float m = -INFINITY;
         if (!(s < INFINITY)) {
-            if (lane == 0) atomicOr(&errors, SV_ERR_SCORE);
+            bad = SV_ERR_SCORE;
         } else if (s > -INFINITY && ended) {
             state = 2;
         } else if (s > -INFINITY) {
-            BeamPart p = {-INFINITY, 0, 0.0};
-            if (lane < a.nc) p = a.part[(size_t)slot * a.nc + lane];
-            m = wave_max(p.m);
-            const double off = beam_offset(m, e);
-            const double sum = wave_sum(p.m == -INFINITY ? p.s : p.s * exp2(beam_offset(p.m, e) - off));
             if (!(sum < INFINITY)) {  // NaN
-                if (lane == 0) atomicOr(&errors, SV_ERR_ROW);
+                bad = SV_ERR_ROW;
             } else if (m > -INFINITY) {
                 state = 1;
-                // ln 2 (log2 sum + off - m c): the offset's rounding comes off again
-                base -= (log2(sum) + (off - (double)m * e.c64)) / kLog2e;
+                // ln 2 (log2 sum + offset - m c): the offset's rounding comes off again
+                base -= (log2(sum) + (beam_offset(m, e) - (double)m * e.c64)) * kLn2;
             }
         }
-        if (lane == 0) {
-            rows.state[w] = state;
-            rows.base[w] = base;
-            rows.m[w] = m;
-        }
+        if (bad && good_t) atomicOr(&errors, bad);
+        rows[w] = {base, m, state};
     }
     __syncthreads();
     float *out_score = a.out_score + (size_t)b * a.M;
@@ -432,58 +510,116 @@ __global__ __launch_bounds__(kBlock) void beam_merge_kernel(const BeamArgs a)
         out_score[r] = (float)order_double(c.c);
         out_parent[r] = c.w;
         out_token[r] = token;
-        if (out_finished) out_finished[r] = (rows.state[c.w] == 2 || token == a.eos) ? 1 : 0;
+        if (out_finished) out_finished[r] = (rows[c.w].state == 2 || token == a.eos) ? 1 : 0;
     };
     if (errors) {
         if (tid == 0 && a.error_word) atomicOr(a.error_word, errors);
     } else {
-        const uint64_t *keys = a.keys + (size_t)b * a.W * a.nc * a.M;
-        const int n = a.W * a.nc * a.M;
         const double inv_t = 1.0 / (double)T;
-        uint64_t best = 0;
-        for (int i = tid; i < n; i += kBlock) best = larger(best, beam_candidate(a, rows, keys, i, inv_t).c);
-        const uint64_t tau = larger(block_kth(best, a.M, lds_k), (uint64_t)1);
-        if (best >= tau)
-            for (int i = tid; i < n; i += kBlock) {
-                const BeamCand c = beam_candidate(a, rows, keys, i, inv_t);
-                if (c.c < tau) continue;
-                const int at = atomicAdd(&cnt, 1);
-                if (at < kBeamKeep) cand[at] = c;
+        // the columns' best candidates, roughly; i / nc for i < 256, nc <= 64 by a product
+        const uint32_t inv_nc = 65536u / (uint32_t)a.nc + 1u;
+        auto row_of = [&](int chunk) { return (int)((uint32_t)chunk * inv_nc >> 16); };
+        const int own = row_of(col0 >> a.cols_log);
+        const BeamRow r = rows[own];
+        const bool alone = r.state == 2 && col0 == (own * a.nc) << a.cols_log;
+        float best = -INFINITY;
+        if (mine && r.state == 1) {
+            float top = x[0];
+#pragma unroll
+            for (int j = 1; j < kBeamPre; ++j) top = fmaxf(top, x[j]);
+            if (top > -INFINITY) best = beam_rough(beam_c(r, top, inv_t));
+        } else if (mine && alone) {
+            best = beam_rough(r.base);
+        }
+        const float tau = fmaxf(block_kth(best, a.M, lds_k), -FLT_MAX);
+        // the floor as a logit of a row, held low enough for every rounding on the way
+        auto floor_of = [&](const BeamRow &r) {
+            const double m = (double)r.m, d = ((double)tau - r.base) * (double)T;
+            return (float)(m + d - 0x1p-20 * (fabs(m) + fabs(d)));
+        };
+        if (best >= tau) {
+            const float least = floor_of(r);
+#pragma unroll
+            for (int j = 0; j < kBeamPre; ++j) {
+                if (j >= per || !(alone ? j == 0 : x[j] >= least && x[j] > -INFINITY)) continue;
+                const int at = atomicAdd(&n_hits, 1);
+                if (at < kBeamHits) hits[at] = col0 + j;
             }
+        }
+        if (tid < a.W) low[tid] = floor_of(rows[tid]);
         __syncthreads();
-        const int k = cnt;
-        if (k <= kBeamKeep) {
-            for (int i = tid; i < k; i += kBlock) {
-                const BeamCand c = cand[i];
+        const int nh = n_hits;
+        if (nh <= kBeamHits) {
+            constexpr int VEC = Elt<DT>::kVec;
+            auto keep = [&](double c, uint64_t key, int w) {
+                const int at = atomicAdd(&n_cand, 1);
+                if (at < kBeamKeep) cand[at] = {double_order(c), key, w};
+            };
+            const int C = 1 << a.cols_log, nv = (a.cvec + C - 1) >> a.cols_log;  // vectors per column
+            for (int i0 = tid; i0 < nh * nv; i0 += kBeamAgain * kMerge) {
+                // every load of a batch is unconditional (the maxima stand in
+                // where there is no vector), so that all are in flight at once
+                BeamLoad<DT, ALIGNED> in[kBeamAgain];
+                int q[kBeamAgain], w[kBeamAgain];
+#pragma unroll
+                for (int j = 0; j < kBeamAgain; ++j) {
+                    const int i = i0 + j * kMerge, h = min(i / nv, nh - 1), v = i - h * nv;
+                    const int col = hits[h], chunk = col >> a.cols_log;
+                    w[j] = row_of(chunk);
+                    const int q0 = (chunk - w[j] * a.nc) * a.cvec;
+                    q[j] = q0 + (col & (C - 1)) + (v << a.cols_log);
+                    const bool none = i >= nh * nv || q[j] >= min(a.nvec, q0 + a.cvec);
+                    if (rows[w[j]].state == 2) {
+                        if (!none && v == 0) keep(rows[w[j]].base, top_key(0.f, a.eos), w[j]);
+                        q[j] = -1;
+                    }
+                    if (none) q[j] = -1;
+                    in[j].issue(q[j] >= 0 ? beam_row(a, b, w[j]) + (size_t)q[j] * 16 : reinterpret_cast<const char *>(cols),
+                               q[j] >= 0 ? min(VEC, a.V - q[j] * VEC) : 1);
+                }
+#pragma unroll
+                for (int j = 0; j < kBeamAgain; ++j) {
+                    if (q[j] < 0) continue;
+                    const uint4 vec = in[j].vector();
+                    float z[VEC];
+                    Elt<DT>::unpack(vec, z);
+                    const float least = low[w[j]];
+                    uint32_t at = 0;  // elements that may reach the floor
+#pragma unroll
+                    for (int k = 0; k < VEC; ++k)
+                        at |= (z[k] >= least && z[k] != -INFINITY && q[j] * VEC + k < a.V) ? 1u << k : 0u;
+                    for (; at; at &= at - 1) {
+                        const int k = __ffs(at) - 1;
+                        const float zk = elt_of<DT>(vec, k);
+                        const double c = beam_c(rows[w[j]], zk, inv_t);
+                        if (beam_rough(c) >= tau) keep(c, top_key(zk, q[j] * VEC + k), w[j]);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        const int k = n_cand;
+        __syncthreads();  // the slow path counts with n_cand too
+        if (nh <= kBeamHits && k <= kBeamKeep) {
+            // distinct candidates: a place is the number of better ones
+            // (eight lanes to a candidate)
+            for (int i0 = 0; i0 < k; i0 += kMerge / 8) {
+                const int i = i0 + tid / 8;
+                const BeamCand c = cand[min(i, k - 1)];
                 int rank = 0;
-                for (int j = 0; j < k; ++j) rank += ahead(cand[j], c);
-                if (rank < a.M) put(rank, c);
+                for (int j = tid % 8; j < k; j += 8) rank += ahead(cand[j], c);
+                rank += lane_xor<1>(rank);
+                rank += lane_xor<2>(rank);
+                rank += lane_xor<4>(rank);
+                if (tid % 8 == 0 && i < k && rank < a.M) put(rank, c);
             }
             found = min(k, a.M);
         } else {
-            // more equal ones than fit: the best behind the last, M times
-            __syncthreads();
-            BeamCand last = {~0ull, ~0ull, -1};
-            for (; found < a.M; ++found) {
-                BeamCand top = {0, 0, INT_MAX};
-                for (int i = tid; i < n; i += kBlock) {
-                    const BeamCand c = beam_candidate(a, rows, keys, i, inv_t);
-                    if (c.c && ahead(last, c) && ahead(c, top)) top = c;
-                }
-                cand[tid] = top;
-                __syncthreads();
-                for (int h = kBlock / 2; h > 0; h >>= 1) {
-                    if (tid < h && ahead(cand[tid + h], cand[tid])) cand[tid] = cand[tid + h];
-                    __syncthreads();
-                }
-                last = cand[0];
-                __syncthreads();
-                if (!last.c) break;
-                if (tid == 0) put(found, last);
-            }
+            found = beam_slow<DT>(a, rows, b, tau, inv_t, cand, reinterpret_cast<uint64_t *>(lds), &n_cand, lds_i);
+            for (int i = tid; i < found; i += kMerge) put(i, cand[i]);
         }
     }
-    for (int r = found + tid; r < a.M; r += kBlock) {
+    for (int r = found + tid; r < a.M; r += kMerge) {
         out_score[r] = -INFINITY;
         out_parent[r] = -1;
         out_token[r] = -1;
@@ -492,12 +628,16 @@ __global__ __launch_bounds__(kBlock) void beam_merge_kernel(const BeamArgs a)
 }
 
 template <int DT>
-static void launch_beam(const BeamArgs &a, bool aligned, hipStream_t s)
+static void launch_beam(const BeamArgs &a, hipStream_t s)
 {
     const unsigned grid = (unsigned)((int64_t)a.B * a.W * a.nc);
-    if (aligned) beam_rows_kernel<DT, true><<<grid, kBlock, 0, s>>>(a);
-    else beam_rows_kernel<DT, false><<<grid, kBlock, 0, s>>>(a);
-    beam_merge_kernel<<<(unsigned)a.B, kBlock, 0, s>>>(a);
+    if (a.aligned) {
+        beam_rows_kernel<DT, true><<<grid, kBlock, 0, s>>>(a);
+        beam_merge_kernel<DT, true><<<(unsigned)a.B, kMerge, 0, s>>>(a);
+    } else {
+        beam_rows_kernel<DT, false><<<grid, kBlock, 0, s>>>(a);
+        beam_merge_kernel<DT, false><<<(unsigned)a.B, kMerge, 0, s>>>(a);
+    }
 }
 
 }  // namespace sv
@@ -540,18 +680,20 @@ int32_t spec_beam_select(const void *logits, int32_t B, int32_t W, int32_t V, in
     a.nvec = p.nvec;
     a.nc = p.nc;
     a.cvec = p.cvec;
-    a.gt = p.gt;
+    a.cols_log = p.cols_log;
+    a.per = p.per;
+    a.g_log = p.g_log;
     a.part = static_cast<sv::BeamPart *>(workspace);
-    a.keys = reinterpret_cast<uint64_t *>(static_cast<char *>(workspace) + p.off_keys);
+    a.cols = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.off_cols);
     a.out_score = out_score;
     a.out_parent = out_parent;
     a.out_token = out_token;
     a.out_finished = out_finished;
     a.error_word = error_word;
-    const bool aligned = ((uintptr_t)logits | (uintptr_t)a.seq_bytes | (uintptr_t)a.beam_bytes) % 16 == 0;
+    a.aligned = ((uintptr_t)logits | (uintptr_t)a.seq_bytes | (uintptr_t)a.beam_bytes) % 16 == 0;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if (dtype == SV_F32) sv::launch_beam<0>(a, aligned, s);
-    else sv::launch_beam<1>(a, aligned, s);
+    if (dtype == SV_F32) sv::launch_beam<0>(a, s);
+    else sv::launch_beam<1>(a, s);
     return hipGetLastError() == hipSuccess ? SV_OK : SV_EHIP;
 }
 

@@ -43,6 +43,12 @@ __device__ __forceinline__ float lane_xor(float v)
 }
 
 template <int MASK>
+__device__ __forceinline__ double lane_xor(double v)
+{
+    return __hiloint2double(lane_xor<MASK>(__double2hiint(v)), lane_xor<MASK>(__double2loint(v)));
+}
+
+template <int MASK>
 __device__ __forceinline__ uint64_t lane_xor(uint64_t v)
 {
     const uint32_t lo = (uint32_t)lane_xor<MASK>((int)(uint32_t)v);
@@ -104,7 +110,8 @@ __device__ __forceinline__ T wave_sort(T v)
     return sort_step<1, 1>(v);
 }
 
-// The k-th largest (1 <= k <= 64) of the values of kBlock threads, one each.
+// The k-th largest (1 <= k <= 64) of the values of the workgroup's first
+// kBlock threads, one each; every thread calls it and gets the result.
 // Every wave sorts its 64; the larger of a descending list and a reversed one
 // are the best 64 of both and bitonic, so two merges leave the best 64 of
 // all.  lds: kBlock + 1 values, free again after the call.
@@ -113,8 +120,7 @@ __device__ __forceinline__ T block_kth(T v, int k, T *lds)
 {
     static_assert(kWaves == 4, "two levels of merges");
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    v = wave_sort(v);
-    lds[threadIdx.x] = v;
+    if (wave < kWaves) lds[threadIdx.x] = v = wave_sort(v);
     __syncthreads();
     if (wave < 2) {
         v = wave_merge(larger(lds[wave * 128 + lane], lds[wave * 128 + 127 - lane]));
