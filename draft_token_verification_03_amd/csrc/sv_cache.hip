@@ -7,7 +7,11 @@
 // per token (page).  One workgroup scans: there are at most a few thousand
 // sequences, and a second workgroup would need a hand-off that costs more
 // than their loads.  Few tokens follow in the same workgroup, so that a
-// decode step is one launch; many get a launch of their own.
+// decode step is one launch; many get a launch of their own.  What bounds a
+// step is dependent memory round trips: lengths, then pages.  Up to kPlan
+// sequences have a thread each, their sums stay in LDS, and then every
+// sequence gets as many lanes as there are to spare for its tokens, so that
+// nothing searches and no trip is added.
 #include <algorithm>
 
 #include "specdecode.h"
@@ -31,45 +35,36 @@ struct CacheArgs {
     int32_t *positions, *seq_ids, *query_start, *granted, *page_start;
     int32_t *error_word;
     int32_t extra, B, max_blocks, page_size, num_pages, max_tokens;
+    uint32_t page_mul, page_shift;  // page_of
 };
 
-__device__ __forceinline__ int64_t wave_scan(int64_t v)
-{
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int64_t w = __shfl_up(v, d);
-        if (lane >= d) v += w;
-    }
-    return v;
-}
-
 // Exclusive prefix sums of two counts over the workgroup, and their totals.
+// Sums stay below 2^20 2^31, which doubles hold exactly.
 struct Sums {
     int64_t a, b, all_a, all_b;
 };
 
-__device__ __forceinline__ Sums plan_scan(int64_t a, int64_t b, int64_t *lds)
+__device__ __forceinline__ Sums plan_scan(int64_t a, int64_t b, double *lds)
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t ia = wave_scan(a), ib = wave_scan(b);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const double ia = wave_inclusive_scan((double)a), ib = wave_inclusive_scan((double)b);
     if (lane == 63) {
         lds[wave] = ia;
         lds[kPlanWaves + wave] = ib;
     }
     __syncthreads();
-    Sums s = {ia - a, ib - b, 0, 0};
-    for (int w = 0; w < kPlanWaves; ++w) {
-        const int64_t x = lds[w], y = lds[kPlanWaves + w];
+    double xa = ia, xb = ib, all_a = 0.0, all_b = 0.0;
+    for (int w = 0; w < waves; ++w) {
+        const double x = lds[w], y = lds[kPlanWaves + w];
         if (w < wave) {
-            s.a += x;
-            s.b += y;
+            xa += x;
+            xb += y;
         }
-        s.all_a += x;
-        s.all_b += y;
+        all_a += x;
+        all_b += y;
     }
     __syncthreads();
-    return s;
+    return {(int64_t)xa - a, (int64_t)xb - b, (int64_t)all_a, (int64_t)all_b};
 }
 
 __device__ __forceinline__ void cache_error(const CacheArgs &a, int bit)
@@ -77,9 +72,17 @@ __device__ __forceinline__ void cache_error(const CacheArgs &a, int bit)
     if (a.error_word) atomicOr(a.error_word, bit);
 }
 
-__device__ __forceinline__ int pages_of(int tokens, int page_size)
+// n / page_size for 0 <= n < 2^31 by a product: with 2^(s-1) < page_size <=
+// 2^s and mul = ceil(2^(31+s) / page_size), n mul >> (31 + s).
+__device__ __forceinline__ int page_of(const CacheArgs &a, int n)
 {
-    return tokens / page_size + (tokens % page_size ? 1 : 0);
+    return (int)(__umulhi(2u * (uint32_t)n, a.page_mul) >> a.page_shift);
+}
+
+__device__ __forceinline__ int pages_of(const CacheArgs &a, int tokens)
+{
+    const int full = page_of(a, tokens);
+    return full + (tokens != full * a.page_size ? 1 : 0);
 }
 
 // The free list's length, held within the list.
@@ -90,6 +93,9 @@ __device__ __forceinline__ int free_pages(const CacheArgs &a)
     if (held != f && threadIdx.x == 0) cache_error(a, SV_ERR_PAGES);
     return held;
 }
+
+constexpr int kTokens = 4;    // per thread where they have a launch of their own
+constexpr int kStaged = 2048;  // sequences whose numbers a workgroup of it copies to LDS
 
 // The last i in [lo, hi) with start[i] <= t (start[lo] <= t).
 __device__ __forceinline__ int find_run(const int32_t *start, int lo, int hi, int t)
@@ -117,100 +123,185 @@ __device__ __forceinline__ NewTokens new_tokens(const CacheArgs &a, int b, bool 
     const int64_t most = (int64_t)a.max_blocks * a.page_size;
     bad = x.len < 0 || n < 0 || x.len + n > most;
     x.n = bad ? 0 : (int)n;
-    x.need = bad ? 0 : pages_of(x.len + x.n, a.page_size) - pages_of(x.len, a.page_size);
+    x.need = bad ? 0 : pages_of(a, x.len + x.n) - pages_of(a, x.len);
     return x;
 }
 
-// Token t (of `total`) of the call; `free` is the free list's length before it.
-__device__ __forceinline__ void place_token(const CacheArgs &a, int t, int total, int lo, int hi, int free)
+// Token i of sequence b (len tokens held, query_start q, page_start p) into
+// place t of the call; `free` is the free list's length before the call.
+__device__ __forceinline__ void place_token(const CacheArgs &a, int t, int b, int i, int len, bool granted, int p,
+                                            int free)
 {
+    const int at = len + i;
     int64_t slot = -1;
-    int at = 0, b = -1;
-    if (t < total) {
-        b = find_run(a.query_start, lo, hi, t);
-        const int len = a.seq_len[b], i = t - a.query_start[b];
-        at = len + i;
-        if (a.granted[b]) {
-            const int block = at / a.page_size, off = at - block * a.page_size;
-            const int first = pages_of(len, a.page_size);
-            int32_t *entry = a.table + (int64_t)b * a.max_blocks + block;
-            int page;
-            if (block >= first) {
-                page = a.free_list[free - 1 - (a.page_start[b] + block - first)];
-                if (off == 0) *entry = page;  // a new page's first token is at its start
-            } else {
-                page = *entry;
-            }
-            if (page >= 0 && page < a.num_pages) slot = (int64_t)page * a.page_size + off;
-            else cache_error(a, SV_ERR_PAGE);
-        }
+    if (granted) {
+        const int block = page_of(a, at), off = at - block * a.page_size;
+        const int first = pages_of(a, len);
+        int32_t *entry = a.table + (int64_t)b * a.max_blocks + block;
+        const bool fresh = block >= first;
+        const int page = *(fresh ? a.free_list + (free - 1 - (p + block - first)) : entry);
+        if (fresh && off == 0) *entry = page;  // a new page's first token is at its start
+        if (page >= 0 && page < a.num_pages) slot = (int64_t)page * a.page_size + off;
+        else cache_error(a, SV_ERR_PAGE);
     }
     a.slots[t] = slot;
     a.positions[t] = at;
     a.seq_ids[t] = b;
 }
 
+__device__ __forceinline__ void no_token(const CacheArgs &a, int t)
+{
+    a.slots[t] = -1;
+    a.positions[t] = 0;
+    a.seq_ids[t] = -1;
+}
+
+// What a sequence with x new tokens before q and p gets.
+struct Grant {
+    bool room, fits;
+};
+
+__device__ __forceinline__ Grant grant(const CacheArgs &a, const NewTokens &x, int64_t q, int64_t p, int free)
+{
+    const bool room = q + x.n <= a.max_tokens;
+    return {room, room && (x.need == 0 || p + x.need <= free)};
+}
+
+// Sequences a workgroup's width at a time, one per thread, the next ones
+// requested while these are scanned; FUSED (one round of them): their tokens too.
 template <bool FUSED>
 __global__ __launch_bounds__(kPlan) void extend_plan_kernel(const CacheArgs a)
 {
-    __shared__ int64_t lds[2 * kPlanWaves];
+    __shared__ double lds[2 * kPlanWaves];
+    __shared__ int4 seqs[FUSED ? kPlan : 1];  // len, query_start, tokens (negative: not granted), page_start
     __shared__ int used;
     const int tid = threadIdx.x;
-    const int run = (a.B + kPlan - 1) / kPlan;  // sequences per thread
-    const int b0 = min(tid * run, a.B), b1 = min(b0 + run, a.B);
+    NewTokens x = {0, 0, 0};
+    bool bad = false;
+    if (tid < a.B) x = new_tokens(a, tid, bad);
     const int free = free_pages(a);
     if (tid == 0) used = 0;
-    int64_t n = 0, need = 0;
-    bool any_bad = false;
-    for (int b = b0; b < b1; ++b) {
-        bool bad;
-        const NewTokens x = new_tokens(a, b, bad);
-        any_bad |= bad;
-        n += x.n;
-        need += x.need;
+    int64_t q0 = 0, p0 = 0;
+    for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
+        const int b = b0 + tid;
+        NewTokens next = {0, 0, 0};
+        bool next_bad = false;
+        if (!FUSED && b + (int)blockDim.x < a.B) next = new_tokens(a, b + blockDim.x, next_bad);
+        const Sums s = plan_scan(x.n, x.need, lds);  // its barriers order `used` too
+        const int64_t qs = q0 + s.a, ps = p0 + s.b;
+        const Grant g = grant(a, x, qs, ps, free);
+        if (b < a.B) {
+            if (g.fits && x.need) atomicMax(&used, (int)(ps + x.need));
+            if (bad || !g.room) cache_error(a, SV_ERR_LENGTH);
+            if (g.room && !g.fits) cache_error(a, SV_ERR_PAGES);
+        }
+        __syncthreads();
+        if (b < a.B) {
+            // behind the sequences that got theirs nothing is taken, so that
+            // `used` is final for whoever it cuts off
+            const int q = (int)min(qs, (int64_t)a.max_tokens), p = (int)min(ps, (int64_t)used);
+            a.query_start[b] = q;
+            a.page_start[b] = p;
+            a.granted[b] = g.fits ? x.n : 0;
+            if (FUSED) {
+                const int here = min(x.n, a.max_tokens - q);
+                seqs[b] = make_int4(x.len, q, g.fits ? here : -here, p);
+            }
+        }
+        q0 += s.all_a;
+        p0 += s.all_b;
+        x = next;
+        bad = next_bad;
     }
-    const Sums s = plan_scan(n, need, lds);  // its barriers order `used` too
-    int64_t q = s.a, p = s.b;
-    int taken = 0;
-    bool lack = false;
-    for (int b = b0; b < b1; ++b) {
-        bool bad;
-        const NewTokens x = new_tokens(a, b, bad);
-        const bool room = q + x.n <= a.max_tokens;
-        const bool fits = room && (x.need == 0 || p + x.need <= free);
-        any_bad |= !room;
-        lack |= room && !fits;
-        a.query_start[b] = (int32_t)min(q, (int64_t)a.max_tokens);
-        a.page_start[b] = (int32_t)min(p, (int64_t)free);
-        a.granted[b] = fits ? x.n : 0;
-        q += x.n;
-        p += x.need;
-        if (fits && x.need) taken = (int)p;
-    }
-    if (taken) atomicMax(&used, taken);
-    if (any_bad) cache_error(a, SV_ERR_LENGTH);
-    if (lack) cache_error(a, SV_ERR_PAGES);
-    __syncthreads();
-    const int total = (int)min(s.all_a, (int64_t)a.max_tokens);
-    // behind the sequences that got theirs nothing is taken
-    for (int b = b0; b < b1; ++b)
-        if (a.page_start[b] > used) a.page_start[b] = used;
+    const int total = (int)min(q0, (int64_t)a.max_tokens);
     if (tid == 0) {
         a.query_start[a.B] = total;
         a.page_start[a.B] = used;
         *a.free_count_out = free - used;
     }
-    if (FUSED) {
-        __syncthreads();
-        for (int t = tid; t < a.max_tokens; t += kPlan) place_token(a, t, total, 0, a.B, free);
+    if (!FUSED) return;
+    __syncthreads();
+    int lanes = 1;  // per sequence
+    while (2 * lanes * a.B <= (int)blockDim.x) lanes *= 2;
+    const int b = tid / lanes;
+    if (b < a.B) {
+        const int4 v = seqs[b];
+        for (int i = tid % lanes; i < abs(v.z); i += lanes) place_token(a, v.y + i, b, i, v.x, v.z > 0, v.w, free);
     }
+    for (int t = total + tid; t < a.max_tokens; t += blockDim.x) no_token(a, t);
 }
 
+// kTokens tokens per thread, a workgroup apart, every step for all of them at
+// once: their sequences, their pages, the stores.  The sequences' numbers are
+// searched and read in LDS where they fit (STAGED): one memory round trip for
+// them all instead of one per step of the search.
+template <bool STAGED>
 __global__ __launch_bounds__(kBlock) void extend_tokens_kernel(const CacheArgs a)
 {
-    const int t = blockIdx.x * kBlock + threadIdx.x;
-    if (t >= a.max_tokens) return;
-    place_token(a, t, a.query_start[a.B], 0, a.B, *a.free_count_out + a.page_start[a.B]);
+    __shared__ int32_t lds[STAGED ? 4 : 1][STAGED ? kStaged : 1];
+    if (STAGED) {
+        for (int i = threadIdx.x; i < a.B; i += kBlock) {
+            lds[0][i] = a.query_start[i];
+            lds[1][i] = a.seq_len[i];
+            lds[2][i] = a.page_start[i];
+            lds[3][i] = a.granted[i];
+        }
+    }
+    const int total = a.query_start[a.B], free = *a.free_count_out + a.page_start[a.B];
+    __syncthreads();
+    const int32_t *start = STAGED ? lds[0] : a.query_start, *lens = STAGED ? lds[1] : a.seq_len;
+    const int32_t *taken = STAGED ? lds[2] : a.page_start, *granted = STAGED ? lds[3] : a.granted;
+    const int64_t t0 = (int64_t)blockIdx.x * (kTokens * kBlock) + threadIdx.x;
+    int t[kTokens], b[kTokens], at[kTokens], off[kTokens], first[kTokens], p[kTokens], page[kTokens];
+    int32_t *entry[kTokens];
+    bool some[kTokens];
+#pragma unroll
+    for (int j = 0; j < kTokens; ++j) {
+        t[j] = (int)min(t0 + j * kBlock, (int64_t)a.max_tokens);
+        some[j] = t[j] < total;
+        b[j] = 0;
+    }
+    for (int step = 1 << (31 - __clz(a.B)); step; step >>= 1)
+#pragma unroll
+        for (int j = 0; j < kTokens; ++j)
+            if (b[j] + step < a.B && start[b[j] + step] <= t[j]) b[j] += step;
+#pragma unroll
+    for (int j = 0; j < kTokens; ++j) {
+        const int len = lens[b[j]];
+        at[j] = len + t[j] - start[b[j]];
+        first[j] = pages_of(a, len);
+        p[j] = taken[b[j]];
+        some[j] = some[j] && granted[b[j]] > 0;
+    }
+#pragma unroll
+    for (int j = 0; j < kTokens; ++j) {
+        const int block = page_of(a, at[j]);
+        off[j] = at[j] - block * a.page_size;
+        const bool fresh = block >= first[j];
+        entry[j] = fresh && off[j] == 0 ? a.table + (int64_t)b[j] * a.max_blocks + block : nullptr;
+        const int32_t *from = fresh ? a.free_list + (free - 1 - (p[j] + block - first[j]))
+                                    : a.table + (int64_t)b[j] * a.max_blocks + block;
+        page[j] = *(some[j] ? from : a.query_start);
+    }
+#pragma unroll
+    for (int j = 0; j < kTokens; ++j) {
+        if (t[j] >= a.max_tokens) continue;
+        if (t[j] >= total) {
+            no_token(a, t[j]);
+            continue;
+        }
+        int64_t slot = -1;
+        if (some[j]) {
+            if (entry[j]) *entry[j] = page[j];
+            if (page[j] >= 0 && page[j] < a.num_pages)
+                slot = (int64_t)page[j] * a.page_size + off[j];
+            else
+                cache_error(a, SV_ERR_PAGE);
+        }
+        a.slots[t[j]] = slot;
+        a.positions[t[j]] = at[j];
+        a.seq_ids[t[j]] = b[j];
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -233,16 +324,15 @@ __device__ __forceinline__ Kept kept_tokens(const CacheArgs &a, int b, bool &bad
         bad = want != keep;
         k.len = len + keep;
     }
-    k.first = pages_of(k.len, a.page_size);
-    k.back = pages_of(len + held, a.page_size) - k.first;
+    k.first = pages_of(a, k.len);
+    k.back = pages_of(a, len + held) - k.first;
     return k;
 }
 
-// Page i of the `total` that come back; the list held `free` before.
-__device__ __forceinline__ void give_page(const CacheArgs &a, int i, int total, int free)
+// Page `block` of sequence b, number i of the `total` that come back; the
+// list held `free` before.
+__device__ __forceinline__ void give_page(const CacheArgs &a, int b, int block, int i, int total, int free)
 {
-    const int b = find_run(a.page_start, 0, a.B, i);
-    const int block = pages_of(a.seq_len_out[b], a.page_size) + i - a.page_start[b];
     int page = a.table[(int64_t)b * a.max_blocks + block];
     if (page < 0 || page >= a.num_pages) {
         cache_error(a, SV_ERR_PAGE);
@@ -251,48 +341,86 @@ __device__ __forceinline__ void give_page(const CacheArgs &a, int i, int total, 
     a.free_list[free + total - 1 - i] = page;
 }
 
+// As extend_plan_kernel; FUSED (one round of sequences): their pages too.
 template <bool FUSED>
 __global__ __launch_bounds__(kPlan) void commit_plan_kernel(const CacheArgs a)
 {
-    __shared__ int64_t lds[2 * kPlanWaves];
+    __shared__ double lds[2 * kPlanWaves];
+    __shared__ int4 seqs[FUSED ? kPlan : 1];  // first block given back, blocks, page_start
     const int tid = threadIdx.x;
-    const int run = (a.B + kPlan - 1) / kPlan;
-    const int b0 = min(tid * run, a.B), b1 = min(b0 + run, a.B);
-    const int free = free_pages(a);
-    int64_t back = 0;
-    bool any_bad = false;
-    for (int b = b0; b < b1; ++b) {
-        bool bad;
-        back += kept_tokens(a, b, bad).back;
-        any_bad |= bad;
+    Kept k = {0, 0, 0};
+    bool bad = false;
+    if (tid < a.B) k = kept_tokens(a, tid, bad);
+    const int free = free_pages(a), room = a.num_pages - free;
+    int64_t p0 = 0;
+    for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
+        const int b = b0 + tid;
+        Kept next = {0, 0, 0};
+        bool next_bad = false;
+        if (!FUSED && b + (int)blockDim.x < a.B) next = kept_tokens(a, b + blockDim.x, next_bad);
+        const Sums s = plan_scan(k.back, 0, lds);
+        const int p = (int)min(p0 + s.a, (int64_t)room);
+        if (b < a.B) {
+            a.page_start[b] = p;
+            a.seq_len_out[b] = k.len;
+            if (FUSED) seqs[b] = make_int4(k.first, min(k.back, room - p), p, 0);
+            if (bad) cache_error(a, SV_ERR_LENGTH);
+        }
+        p0 += s.all_a;
+        k = next;
+        bad = next_bad;
     }
-    const Sums s = plan_scan(back, 0, lds);
-    const int room = a.num_pages - free;
-    const int total = (int)min(s.all_a, (int64_t)room);
-    int64_t p = s.a;
-    for (int b = b0; b < b1; ++b) {
-        bool bad;
-        const Kept k = kept_tokens(a, b, bad);
-        a.page_start[b] = (int32_t)min(p, (int64_t)room);
-        a.seq_len_out[b] = k.len;
-        p += k.back;
-    }
-    if (any_bad) cache_error(a, SV_ERR_LENGTH);
+    const int total = (int)min(p0, (int64_t)room);
     if (tid == 0) {
-        if (s.all_a > room) cache_error(a, SV_ERR_PAGES);
+        if (p0 > room) cache_error(a, SV_ERR_PAGES);
         a.page_start[a.B] = total;
         *a.free_count_out = free + total;
     }
-    if (FUSED) {
-        __syncthreads();
-        for (int i = tid; i < total; i += kPlan) give_page(a, i, total, free);
+    if (!FUSED) return;
+    __syncthreads();
+    int lanes = 1;  // per sequence
+    while (2 * lanes * a.B <= (int)blockDim.x) lanes *= 2;
+    const int b = tid / lanes;
+    if (b < a.B) {
+        const int4 v = seqs[b];
+        for (int i = tid % lanes; i < v.y; i += lanes) give_page(a, b, v.x + i, v.z + i, total, free);
     }
 }
 
+template <bool STAGED>
 __global__ __launch_bounds__(kBlock) void commit_pages_kernel(const CacheArgs a)
 {
+    __shared__ int32_t lds[STAGED ? 2 : 1][STAGED ? kStaged : 1];
     const int total = a.page_start[a.B], free = *a.free_count_out - total;
-    for (int i = blockIdx.x * kBlock + threadIdx.x; i < total; i += gridDim.x * kBlock) give_page(a, i, total, free);
+    if ((int64_t)blockIdx.x * kBlock >= total) return;
+    if (STAGED) {
+        for (int i = threadIdx.x; i < a.B; i += kBlock) {
+            lds[0][i] = a.page_start[i];
+            lds[1][i] = a.seq_len_out[i];
+        }
+    }
+    __syncthreads();
+    const int32_t *start = STAGED ? lds[0] : a.page_start, *lens = STAGED ? lds[1] : a.seq_len_out;
+    for (int i = blockIdx.x * kBlock + threadIdx.x; i < total; i += gridDim.x * kBlock) {
+        const int b = find_run(start, 0, a.B, i);
+        give_page(a, b, pages_of(a, lens[b]) + i - start[b], i, total, free);
+    }
+}
+
+// Threads of the scanning workgroup: one per sequence, and enough for `work`.
+static unsigned plan_threads(int32_t B, int64_t work)
+{
+    unsigned n = 256;
+    while (n < (unsigned)kPlan && (n < (unsigned)B || n < work)) n *= 2;
+    return n;
+}
+
+static void set_page_size(CacheArgs &a, int32_t page_size)
+{
+    a.page_size = page_size;
+    a.page_shift = 0;
+    while (((int64_t)1 << a.page_shift) < page_size) ++a.page_shift;
+    a.page_mul = (uint32_t)((((uint64_t)1 << (31 + a.page_shift)) + page_size - 1) / page_size);
 }
 
 static bool cache_ok(int32_t B, int32_t max_blocks, int32_t page_size, int32_t num_pages)
@@ -324,7 +452,7 @@ int32_t spec_cache_extend(const int32_t *seq_len, const int32_t *new_len, int32_
     a.B = B;
     a.table = block_table;
     a.max_blocks = max_blocks;
-    a.page_size = page_size;
+    sv::set_page_size(a, page_size);
     a.free_list = const_cast<int32_t *>(free_list);
     a.num_pages = num_pages;
     a.free_count = free_count;
@@ -338,11 +466,14 @@ int32_t spec_cache_extend(const int32_t *seq_len, const int32_t *new_len, int32_
     a.page_start = page_start;
     a.error_word = error_word;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if (max_tokens <= sv::kFusedTokens) {
-        sv::extend_plan_kernel<true><<<1, sv::kPlan, 0, s>>>(a);
-    } else {
-        sv::extend_plan_kernel<false><<<1, sv::kPlan, 0, s>>>(a);
-        sv::extend_tokens_kernel<<<(unsigned)(((int64_t)max_tokens + sv::kBlock - 1) / sv::kBlock), sv::kBlock, 0, s>>>(a);
+    const bool fused = B <= sv::kPlan && max_tokens <= sv::kFusedTokens;
+    if (fused) sv::extend_plan_kernel<true><<<1, sv::plan_threads(B, max_tokens), 0, s>>>(a);
+    else sv::extend_plan_kernel<false><<<1, sv::plan_threads(B, 0), 0, s>>>(a);
+    if (!fused && max_tokens > 0) {
+        const int64_t per = sv::kBlock * sv::kTokens;
+        const unsigned grid = (unsigned)((max_tokens + per - 1) / per);
+        if (B <= sv::kStaged) sv::extend_tokens_kernel<true><<<grid, sv::kBlock, 0, s>>>(a);
+        else sv::extend_tokens_kernel<false><<<grid, sv::kBlock, 0, s>>>(a);
     }
     return hipGetLastError() == hipSuccess ? SV_OK : SV_EHIP;
 }
@@ -367,7 +498,7 @@ int32_t spec_cache_commit(const int32_t *seq_len, const int32_t *reserved, const
     a.B = B;
     a.table = const_cast<int32_t *>(block_table);
     a.max_blocks = max_blocks;
-    a.page_size = page_size;
+    sv::set_page_size(a, page_size);
     a.free_list = free_list;
     a.num_pages = num_pages;
     a.free_count = free_count;
@@ -376,13 +507,14 @@ int32_t spec_cache_commit(const int32_t *seq_len, const int32_t *reserved, const
     a.page_start = page_start;
     a.error_word = error_word;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if (!finished || (int64_t)B * max_blocks <= sv::kFusedPages) {
-        sv::commit_plan_kernel<true><<<1, sv::kPlan, 0, s>>>(a);
-    } else {
-        sv::commit_plan_kernel<false><<<1, sv::kPlan, 0, s>>>(a);
+    const bool fused = B <= sv::kPlan && (!finished || (int64_t)B * max_blocks <= sv::kFusedPages);
+    if (fused) sv::commit_plan_kernel<true><<<1, sv::plan_threads(B, B), 0, s>>>(a);
+    else sv::commit_plan_kernel<false><<<1, sv::plan_threads(B, 0), 0, s>>>(a);
+    if (!fused) {
         const int64_t most = std::min<int64_t>((int64_t)B * max_blocks, num_pages);
         const unsigned grid = (unsigned)std::min<int64_t>((most + sv::kBlock - 1) / sv::kBlock, 1024);
-        if (grid) sv::commit_pages_kernel<<<grid, sv::kBlock, 0, s>>>(a);
+        if (grid && B <= sv::kStaged) sv::commit_pages_kernel<true><<<grid, sv::kBlock, 0, s>>>(a);
+        else if (grid) sv::commit_pages_kernel<false><<<grid, sv::kBlock, 0, s>>>(a);
     }
     return hipGetLastError() == hipSuccess ? SV_OK : SV_EHIP;
 }

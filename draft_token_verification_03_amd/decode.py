@@ -61,8 +61,9 @@ class _Bound:
     """A call of one entry point: function, arguments, device and stream."""
 
     def _bind(self, device, stream):
-        from . import load_library
+        from . import _check, load_library
         self._lib = load_library()
+        self._check = _check
         self._device = device
         self._stream = torch.cuda.current_stream(device) if stream is None else stream
         if self._stream.device != device:
@@ -74,12 +75,13 @@ class _Bound:
             return (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=self._device)
 
     def _run(self) -> None:
-        from . import _check
         if torch.cuda.current_device() == self._device.index:
-            _check(self._fn(*self._args))
+            status = self._fn(*self._args)
         else:
             with torch.cuda.device(self._device):
-                _check(self._fn(*self._args))
+                status = self._fn(*self._args)
+        if status:
+            self._check(status)
 
 
 class BeamSelector(_Bound):

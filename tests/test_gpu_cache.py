@@ -43,7 +43,8 @@ def setup(rng, B, page, blocks, spare, lengths):
 
 
 EXTEND = [(1, 1, 4, 4, 100), (5, 16, 8, 6, 100), (64, 16, 32, 7, 100), (300, 8, 20, 33, 100), (1500, 4, 12, 5, 100),
-          (7, 64, 40, 2000, 100), (40, 16, 100, 900, 100), (20, 16, 30, 40, 30), (50, 1, 60, 8, 50), (3, 5, 7, 0, 0)]
+          (7, 64, 40, 2000, 100), (40, 16, 100, 900, 100), (20, 16, 30, 40, 30), (50, 1, 60, 8, 50), (3, 5, 7, 0, 0), (1024, 8, 9, 12, 90),
+          (1025, 8, 9, 12, 100), (5000, 4, 12, 5, 100), (2, 128, 200, 20000, 100)]
 
 
 @pytest.mark.parametrize("B,page,blocks,most,share", EXTEND)
@@ -103,7 +104,7 @@ def test_extend_bad_pages_and_counts(sv):
 
 
 COMMIT = [(1, 1, 4, 4, 0.0), (5, 16, 8, 6, 0.0), (64, 16, 32, 7, 0.3), (300, 8, 20, 33, 0.1), (1500, 4, 50, 9, 0.2),
-          (2000, 16, 40, 8, 0.05), (3, 64, 9, 500, 1.0)]
+          (2000, 16, 40, 8, 0.05), (3, 64, 9, 500, 1.0), (1024, 8, 100, 20, 0.4), (1025, 8, 9, 12, 0.5), (5000, 4, 20, 5, 0.1)]
 
 
 @pytest.mark.parametrize("B,page,blocks,most,ended", COMMIT)
