@@ -24,7 +24,8 @@ struct MoveArgs {
     int32_t row_vecs;         // vectors per row
     int32_t num_pages, max_blocks, max_length;
     int32_t N, first;
-    int32_t chunks;           // workgroups per (pool, sequence, group)
+    int32_t chunks;           // workgroups per (pool, sequence, group), or per sequence
+    int32_t pools;            // of this launch
 };
 
 __device__ __forceinline__ void move_error(const MoveArgs &a, int bit)
@@ -87,7 +88,7 @@ __global__ __launch_bounds__(kBlock) void reorder_dense_kernel(const MoveArgs a)
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int64_t v = v0 + i * kBlock + threadIdx.x;
-                if (v < n) x[s][i] = base[s * beam + v];
+                if (v < n) x[s][i] = __builtin_nontemporal_load(&base[s * beam + v]);
             }
 #pragma unroll
     for (int s = 0; s < WM; ++s)
@@ -96,7 +97,7 @@ __global__ __launch_bounds__(kBlock) void reorder_dense_kernel(const MoveArgs a)
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int64_t v = v0 + i * kBlock + threadIdx.x;
-                if (v < n) base[j * beam + v] = x[s][i];
+                if (v < n) __builtin_nontemporal_store(x[s][i], &base[j * beam + v]);
             }
         }
 }
@@ -144,7 +145,7 @@ __global__ __launch_bounds__(kBlock) void reorder_paged_kernel(const MoveArgs a)
             bad = true;
             page[s] = -1;
         } else {
-            x[s] = base[page[s] * page_vecs];
+            x[s] = __builtin_nontemporal_load(&base[page[s] * page_vecs]);
         }
     }
 #pragma unroll
@@ -153,7 +154,7 @@ __global__ __launch_bounds__(kBlock) void reorder_paged_kernel(const MoveArgs a)
         for (uint32_t to = m.to[s]; to; to &= to - 1) {
             const int p = table[(int64_t)(__ffs(to) - 1) * a.max_blocks];
             if (p < 0 || p >= a.num_pages) bad = true;
-            else if (p != page[s]) base[p * page_vecs] = x[s];
+            else if (p != page[s]) __builtin_nontemporal_store(x[s], &base[p * page_vecs]);
         }
     }
     if (bad) move_error(a, SV_ERR_PAGE);
@@ -165,60 +166,64 @@ __global__ __launch_bounds__(kBlock) void reorder_paged_kernel(const MoveArgs a)
 // destination, so a thread that reads ahead of its writes reads what was
 // there before the call.
 
-constexpr int kPathAhead = 4;  // rows read before the first of them is written
+constexpr int kMaxPath = 128;
+constexpr int kPathAhead = 8;  // rows read before the first of them is written
 
+// A workgroup takes kBlock vectors of one position of one sequence, of all
+// pools behind each other.  Its first threads turn the path into row offsets
+// (one round trip for the path, one for the tables), the rest is copies.
 template <class T>
 __global__ __launch_bounds__(kBlock) void compact_kernel(const MoveArgs a)
 {
-    int blk = blockIdx.x;
-    const int chunk = blk % a.chunks;
-    blk /= a.chunks;
-    const int b = blk % a.B, pool = blk / a.B;
+    __shared__ int64_t from[kMaxPath], to[kMaxPath];  // vectors from a column's start; to < 0: stays
+    __shared__ int errors;
+    const int chunk = blockIdx.x % a.chunks, b = blockIdx.x / a.chunks, tid = threadIdx.x;
     const int d = a.accepted[b];
     if (d <= 0) return;
-    const int lane = threadIdx.x & 63;
-    const int32_t *path = a.path + (int64_t)b * a.N;
-    bool bad = d > a.N;
-    for (int i = lane; i < d && !bad; i += 64) {
-        const int p = path[i];
-        bad = p >= a.N || p <= (i ? path[i - 1] : -1);
-    }
-    if (__ballot(bad) != 0ull) {
-        if (threadIdx.x == 0) move_error(a, SV_ERR_TREE);
+    if (d > a.N) {
+        if (tid == 0) move_error(a, SV_ERR_TREE);
         return;
     }
-    const int len = a.length[b];
-    const int64_t base = (int64_t)len + a.first;
-    if (len < 0 || base + path[d - 1] >= (int64_t)a.max_blocks * a.S) {
-        if (threadIdx.x == 0) move_error(a, SV_ERR_LENGTH);
-        return;
-    }
-    const int v = chunk * kBlock + (int)threadIdx.x;
-    const int g = v / a.row_vecs;
-    if (g >= a.G) return;
-    const int32_t *table = a.table + (int64_t)b * a.max_blocks;
+    if (tid == 0) errors = 0;
+    __syncthreads();
     const int64_t page_vecs = (int64_t)a.G * a.S * a.row_vecs;
-    T *col = reinterpret_cast<T *>(a.pool[pool]) + (int64_t)g * a.S * a.row_vecs + (v - g * a.row_vecs);
-    for (int i0 = 0; i0 < d; i0 += kPathAhead) {
-        T x[kPathAhead];
-        T *to[kPathAhead];
-#pragma unroll
-        for (int k = 0; k < kPathAhead; ++k) {
-            to[k] = nullptr;
-            const int i = i0 + k;
-            if (i >= d || path[i] == i) continue;
-            const int from = (int)base + path[i], dest = (int)base + i;
-            const int pf = table[from / a.S], pd = table[dest / a.S];
+    if (tid < d) {
+        const int32_t *path = a.path + (int64_t)b * a.N, *table = a.table + (int64_t)b * a.max_blocks;
+        const int p = path[tid], before = tid ? path[tid - 1] : -1, len = a.length[b];
+        const int64_t base = (int64_t)len + a.first, most = (int64_t)a.max_blocks * a.S;
+        int bad = p >= a.N || p <= before ? SV_ERR_TREE : len < 0 || base + p >= most ? SV_ERR_LENGTH : 0;
+        if (bad) atomicOr(&errors, bad);
+        from[tid] = 0;
+        to[tid] = -1;
+        if (!bad && p != tid && base + tid < most) {
+            const int at = (int)base + p, dest = (int)base + tid;
+            const int pf = table[at / a.S], pd = table[dest / a.S];
             if (pf < 0 || pf >= a.num_pages || pd < 0 || pd >= a.num_pages) {
-                if (threadIdx.x == 0) move_error(a, SV_ERR_PAGE);
-                continue;
+                move_error(a, SV_ERR_PAGE);
+            } else {
+                from[tid] = pf * page_vecs + (int64_t)(at % a.S) * a.row_vecs;
+                to[tid] = pd * page_vecs + (int64_t)(dest % a.S) * a.row_vecs;
             }
-            to[k] = col + pd * page_vecs + (int64_t)(dest % a.S) * a.row_vecs;
-            x[k] = col[pf * page_vecs + (int64_t)(from % a.S) * a.row_vecs];
         }
+    }
+    __syncthreads();
+    if (errors) {  // the sequence stays as it is
+        if (tid == 0) move_error(a, errors);
+        return;
+    }
+    const int64_t v = (int64_t)chunk * kBlock + tid;
+    const int cols = a.G * a.row_vecs, pool = (int)(v / cols);
+    if (pool >= a.pools) return;
+    const int c = (int)(v - (int64_t)pool * cols), g = c / a.row_vecs;
+    T *col = reinterpret_cast<T *>(a.pool[pool]) + (int64_t)g * a.S * a.row_vecs + (c - g * a.row_vecs);
+    for (int i0 = 0; i0 < d; i0 += kPathAhead) {
+        // all loads of a batch are in flight together; a row that stays reads its pool's first
+        T x[kPathAhead];
+#pragma unroll
+        for (int k = 0; k < kPathAhead; ++k) x[k] = col[from[min(i0 + k, d - 1)]];
 #pragma unroll
         for (int k = 0; k < kPathAhead; ++k)
-            if (to[k]) *to[k] = x[k];
+            if (i0 + k < d && to[i0 + k] >= 0) col[to[i0 + k]] = x[k];
     }
 }
 
@@ -258,20 +263,9 @@ static void launch_reorder(const MoveArgs &a, int n, hipStream_t s)
 }
 
 template <class T>
-static void launch_compact(const MoveArgs &a, int n, hipStream_t s)
+static void launch_compact(const MoveArgs &a, hipStream_t s)
 {
-    compact_kernel<T><<<(unsigned)((int64_t)n * a.B * a.chunks), kBlock, 0, s>>>(a);
-}
-
-// Chunks of the positions of one (pool, sequence, group), kBlock * NV vectors
-// each; 0 when the launch would be too large.
-static bool move_grid(MoveArgs &a, int32_t n_pools, int64_t vecs, int per_thread)
-{
-    const int64_t per = (int64_t)kBlock * per_thread;
-    const int64_t chunks = std::max<int64_t>(1, (vecs + per - 1) / per);
-    if (chunks >= ((int64_t)1 << 31) / std::min(n_pools, kMovePools) / a.B / a.G) return false;
-    a.chunks = (int32_t)chunks;
-    return true;
+    compact_kernel<T><<<(unsigned)((int64_t)a.B * a.chunks), kBlock, 0, s>>>(a);
 }
 
 enum Move { kReorder, kCompact };
@@ -280,31 +274,28 @@ static int32_t move_launch(MoveArgs &a, Move what, void *const *pools, int32_t n
                            int64_t positions, hipStream_t s)
 {
     const int vb = move_vector(pools, n_pools, row_bytes);
-    if (row_bytes / vb >= ((int64_t)1 << 31)) return SV_EINVAL;
     a.row_vecs = (int32_t)(row_bytes / vb);
+    const int64_t most = ((int64_t)1 << 31) - kBlock;
+    // workgroups: per (pool, sequence, group) for the positions of a beam, or
+    // per sequence for the vectors of a position in all pools
     const int nv = what == kReorder && !a.table ? (a.W <= 4 ? 4 : a.W <= 8 ? 2 : 1) : 1;
-    if (what == kCompact) {
-        // a thread's column is a vector of one of the G rows of a position
-        if ((int64_t)a.G * a.row_vecs >= ((int64_t)1 << 31) - kBlock) return SV_EINVAL;
-        const int32_t G = a.G;
-        a.G = 1;
-        const bool ok = move_grid(a, n_pools, (int64_t)G * a.row_vecs, 1);
-        a.G = G;
-        if (!ok) return SV_EINVAL;
-    } else if (!move_grid(a, n_pools, positions * a.row_vecs, nv)) {
-        return SV_EINVAL;
-    }
+    const int64_t each = what == kReorder ? positions * a.row_vecs : (int64_t)a.G * a.row_vecs;
+    if (what == kCompact && each >= most) return SV_EINVAL;
     for (int32_t p0 = 0; p0 < n_pools; p0 += kMovePools) {
-        const int n = std::min(kMovePools, n_pools - p0);
-        for (int i = 0; i < n; ++i) a.pool[i] = static_cast<char *>(pools[p0 + i]);
+        a.pools = std::min(kMovePools, n_pools - p0);
+        const int64_t vecs = what == kReorder ? each : each * a.pools, per = (int64_t)kBlock * nv;
+        const int64_t chunks = std::max<int64_t>(1, (vecs + per - 1) / per);
+        if (chunks > most / a.B / (what == kReorder ? a.pools * (int64_t)a.G : 1)) return SV_EINVAL;
+        a.chunks = (int32_t)chunks;
+        for (int i = 0; i < a.pools; ++i) a.pool[i] = static_cast<char *>(pools[p0 + i]);
         if (what == kReorder) {
-            if (vb == 16) launch_reorder<u32x4>(a, n, s);
-            else if (vb == 4) launch_reorder<uint32_t>(a, n, s);
-            else launch_reorder<uint8_t>(a, n, s);
+            if (vb == 16) launch_reorder<u32x4>(a, a.pools, s);
+            else if (vb == 4) launch_reorder<uint32_t>(a, a.pools, s);
+            else launch_reorder<uint8_t>(a, a.pools, s);
         } else {
-            if (vb == 16) launch_compact<u32x4>(a, n, s);
-            else if (vb == 4) launch_compact<uint32_t>(a, n, s);
-            else launch_compact<uint8_t>(a, n, s);
+            if (vb == 16) launch_compact<u32x4>(a, s);
+            else if (vb == 4) launch_compact<uint32_t>(a, s);
+            else launch_compact<uint8_t>(a, s);
         }
     }
     return hipGetLastError() == hipSuccess ? SV_OK : SV_EHIP;
@@ -312,7 +303,7 @@ static int32_t move_launch(MoveArgs &a, Move what, void *const *pools, int32_t n
 
 static bool paged_ok(int32_t G, int32_t page_size, int64_t row_bytes, int32_t num_pages, int32_t max_blocks)
 {
-    return G >= 1 && page_size >= 1 && row_bytes >= 1 && num_pages >= 0 && max_blocks >= 1 &&
+    return G >= 1 && page_size >= 1 && row_bytes >= 1 && num_pages >= 1 && max_blocks >= 1 &&
            (int64_t)max_blocks * page_size < ((int64_t)1 << 31) && row_bytes < ((int64_t)1 << 31) &&
            (double)num_pages * G * page_size * (double)row_bytes < 0x1p62;
 }
@@ -376,7 +367,7 @@ int32_t spec_cache_compact(void *const *pools, int32_t n_pools, int32_t B, int32
                            const int32_t *seq_len, int32_t first, const int32_t *path,
                            const int32_t *accepted_len, int32_t N, int32_t *error_word, void *stream)
 {
-    if (n_pools < 0 || n_pools > SV_MAX_POOLS || B < 0 || N < 0 || N > 128 || first < 0 ||
+    if (n_pools < 0 || n_pools > SV_MAX_POOLS || B < 0 || N < 0 || N > sv::kMaxPath || first < 0 ||
         !sv::paged_ok(G, page_size, row_bytes, num_pages, max_blocks))
         return SV_EINVAL;
     if (B == 0 || n_pools == 0 || N == 0) return SV_OK;

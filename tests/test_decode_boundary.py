@@ -71,7 +71,7 @@ def test_reorder_refusals(sv):
     call = caller(lib, "spec_beam_reorder_paged", "p n B W G ps row np tab mb par st len ml err stream",
                   dict(p=pools(A), n=1, B=2, W=4, G=1, ps=16, row=256, np=100, tab=A, mb=10, par=A, st=None, len=A,
                        ml=160, err=None, stream=None))
-    for bad in (dict(n=1025), dict(B=-1), dict(W=33), dict(G=0), dict(ps=0), dict(row=0), dict(np=-1), dict(tab=None),
+    for bad in (dict(n=1025), dict(B=-1), dict(W=33), dict(G=0), dict(ps=0), dict(row=0), dict(np=0), dict(tab=None),
                 dict(mb=0), dict(mb=1 << 28), dict(par=None), dict(len=None), dict(ml=161), dict(ml=-1), dict(p=None)):
         assert call(**bad) == sv.SV_EINVAL, bad
     for none in (dict(B=0, p=None, par=None), dict(n=0, p=None), dict(ml=0)):
@@ -98,7 +98,7 @@ def test_cache_refusals(sv):
     call = caller(lib, "spec_cache_compact", "p n B G ps row np tab mb sl first path ac N err stream",
                   dict(p=pools(A), n=1, B=2, G=1, ps=16, row=256, np=100, tab=A, mb=10, sl=A, first=1, path=A, ac=A, N=5,
                        err=None, stream=None))
-    for bad in (dict(n=-1), dict(B=-1), dict(G=0), dict(ps=0), dict(row=0), dict(np=-1), dict(mb=0), dict(N=129),
+    for bad in (dict(n=-1), dict(B=-1), dict(G=0), dict(ps=0), dict(row=0), dict(np=0), dict(mb=0), dict(N=129),
                 dict(N=-1), dict(first=-1), dict(p=None), dict(p=pools(None)), dict(tab=None), dict(sl=None),
                 dict(path=None), dict(ac=None)):
         assert call(**bad) == sv.SV_EINVAL, bad
