@@ -31,7 +31,7 @@ namespace sv {
 
 constexpr double kLn2 = 0.6931471805599453;
 constexpr int kBeamLoads = 4;        // 16-byte vectors per thread per tile
-constexpr int kBeamFill = 768;       // workgroups the streaming grid aims for
+constexpr int kBeamFill = 512;       // workgroups the streaming grid aims for: two per CU
 constexpr int kBeamMaxChunks = 64;   // chunks per row: the merge gives each a lane
 constexpr int kBeamRowChunks = 256;  // W * chunks at most: with lanes to spare, one thread each in the merge
 constexpr int kBeamPre = 8;          // column maxima per thread of the merge
