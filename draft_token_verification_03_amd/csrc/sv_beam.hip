@@ -14,10 +14,11 @@
 // so the merge turns the maxima into c and takes the M-th largest over all
 // columns of the sequence as a floor: M columns hold a candidate at least as
 // large each, so no smaller one is among the best M.  Only the columns whose
-// maximum reaches the floor, about M, are read again, all at once; what
-// reaches the floor there is ranked by counting.  A sequence has between 1024
-// and 2048 columns (fewer for short rows): the merge holds eight a thread, and
-// more columns leave less to read again.
+// maximum reaches the floor, about M, are read again, all at once, and of a
+// long one only the tile that held its maximum where the pass saw that no
+// other tile of it reaches the floor; what reaches the floor there is ranked by
+// counting.  A sequence has between 1024 and 2048 columns (fewer for short
+// rows): the merge holds eight a thread, and more leave less to read again.
 #include <algorithm>
 #include <cfloat>
 
@@ -38,6 +39,7 @@ constexpr int kBeamPre = 8;          // column maxima per thread of the merge
 constexpr int kMerge = 1024;         // threads of the merge: 256 hold columns, all of them read columns again
 constexpr int kBeamAgain = 2;        // vectors each requests at once
 constexpr int kBeamHits = 256;       // columns read again
+constexpr int kBeamLong = 40;        // vectors from which on a column is read again by its hint
 constexpr int kBeamKeep = 512;       // candidates ranked at once
 constexpr int kBeamRound = 256;      // vectors the slow path takes at once
 constexpr int kBeamSlow = kBeamRound * 8 + SV_MAX_CANDIDATES;  // their keys and the best so far
@@ -48,6 +50,13 @@ struct BeamPart {
     double s;    // sum of exp2(z c - offset(m)) over the chunk; NaN for NaN or +inf logits
 };
 
+// Of a column: the vector at which its maximum's tile starts for the lane that
+// had it (kBeamLoads vectors, kBlock apart), and the maximum of its other tiles.
+struct BeamHint {
+    float other;
+    int32_t q;
+};
+
 struct BeamArgs {
     const char *logits;
     const float *scores, *temperature;
@@ -55,15 +64,17 @@ struct BeamArgs {
     int64_t seq_bytes, beam_bytes;
     int32_t B, W, V, M, eos, nvec, nc, cvec, cols_log, aligned;
     int32_t per, g_log;  // the merge: columns per thread, 1 << g_log >= nc lanes per row
+    int32_t nv, hinted;  // vectors per column; whether they are enough for hints
     BeamPart *part;     // [B][W][nc]
     float *cols;        // [B][W][nc][1 << cols_log] column maxima
+    BeamHint *hints;    // the same
     float *out_score;
     int32_t *out_parent, *out_token, *out_finished, *error_word;
 };
 
 struct BeamPlan {
     int32_t nvec, nc, cvec, cols_log, per, g_log;
-    size_t off_cols, bytes;
+    size_t off_cols, off_hints, bytes;
 };
 
 static bool make_beam_plan(int32_t B, int32_t W, int32_t V, int32_t dtype, int32_t M, BeamPlan *p)
@@ -88,7 +99,8 @@ static bool make_beam_plan(int32_t B, int32_t W, int32_t V, int32_t dtype, int32
     while (1 << p->g_log < p->nc) ++p->g_log;
     auto align = [](size_t x) { return (x + 255) & ~(size_t)255; };
     p->off_cols = align(sizeof(BeamPart) * (size_t)(rows * p->nc));
-    p->bytes = align(p->off_cols + sizeof(float) * (size_t)((rows * p->nc) << p->cols_log));
+    p->off_hints = align(p->off_cols + sizeof(float) * (size_t)((rows * p->nc) << p->cols_log));
+    p->bytes = align(p->off_hints + sizeof(BeamHint) * (size_t)((rows * p->nc) << p->cols_log));
     return true;
 }
 
@@ -169,47 +181,21 @@ __device__ __forceinline__ float beam_tile(const uint4 (&r)[U], const ExpScale &
     return lm;
 }
 
-template <int DT, bool ALIGNED>
-__device__ __forceinline__ void beam_chunk(const BeamArgs &a, const char *row, int slot, int chunk, float T)
-{
-    constexpr int U = kBeamLoads;
-    __shared__ float lds_col[kBlock], lds_m[kWaves];
-    __shared__ double lds_s[kWaves];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int q0 = chunk * a.cvec, q1 = min(a.nvec, q0 + a.cvec);
-    PairTileU<U> ra;
-    issue_pair<DT, ALIGNED, false>(row, nullptr, q0, q1, a.V, ra);
-    const ExpScale e = make_scale(T);
-    BeamRun run = {-INFINITY, -INFINITY, false, 0.0};
-    float best = -INFINITY;
-    stream_pair<DT, ALIGNED, false>(row, nullptr, q0, q1, a.V, ra, [&](const PairTileU<U> &r, int) {
-        best = fmaxf(best, beam_tile<DT, U>(r.t, e, run));
-    });
-    const double s = wave_sum(run.s);  // against the wave's maximum
-    // column l of C: threads l, l + C, ...
-    const int C = 1 << a.cols_log;
-    if (C < 64) best = fmaxf(best, lane_xor<32>(best));
-    if (C < 32) best = fmaxf(best, lane_xor<16>(best));
-    if (C < 16) best = fmaxf(best, lane_xor<8>(best));
-    lds_col[threadIdx.x] = best;
-    if (lane == 0) {
-        lds_m[wave] = run.m;
-        lds_s[wave] = s;
+struct BeamColumn {
+    float best, other;
+    int q;
+    __device__ __forceinline__ void join(float b, float o, int at)
+    {
+        other = fmaxf(fmaxf(other, o), fminf(best, b));
+        q = b > best ? at : q;
+        best = fmaxf(best, b);
     }
-    __syncthreads();
-    const size_t at = (size_t)slot * a.nc + chunk;
-    if ((int)threadIdx.x < C) {
-        for (int i = max(C, 64); i < kBlock; i += max(C, 64)) best = fmaxf(best, lds_col[threadIdx.x + i]);
-        a.cols[(at << a.cols_log) + threadIdx.x] = best;
+    template <int MASK>
+    __device__ __forceinline__ void join_lane()
+    {
+        join(lane_xor<MASK>(best), lane_xor<MASK>(other), lane_xor<MASK>(q));
     }
-    if (wave != 0) return;
-    const float top = fmaxf(fmaxf(lds_m[0], lds_m[1]), fmaxf(lds_m[2], lds_m[3]));
-    double sum = 0.0;
-    if (lane < kWaves) sum = beam_rebase(lds_s[lane], lds_m[lane], top, e);
-    sum += dpp_double<kDppQuadXor1>(sum);
-    sum += dpp_double<kDppQuadXor2>(sum);
-    if (lane == 0) a.part[at] = {top, 0, sum};
-}
+};
 
 __device__ __forceinline__ const char *beam_row(const BeamArgs &a, int b, int w)
 {
@@ -225,14 +211,66 @@ __device__ __forceinline__ bool beam_live(const BeamArgs &a, int slot)
     return s > -INFINITY && s < INFINITY && !(a.finished && a.finished[slot]);
 }
 
+// The first tile is requested before the beam's score and temperature are
+// known, so the stream starts a round trip earlier; a dead beam wastes it.
 template <int DT, bool ALIGNED>
 __global__ __launch_bounds__(kBlock) void beam_rows_kernel(const BeamArgs a)
 {
+    constexpr int U = kBeamLoads;
+    __shared__ float lds_best[kBlock], lds_other[kBlock], lds_m[kWaves];
+    __shared__ int lds_q[kBlock];
+    __shared__ double lds_s[kWaves];
     const int slot = blockIdx.x / a.nc, chunk = blockIdx.x % a.nc;
-    const int b = slot / a.W, w = slot % a.W;
+    const int b = slot / a.W, w = slot % a.W, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const char *row = beam_row(a, b, w);
+    const int q0 = chunk * a.cvec, q1 = min(a.nvec, q0 + a.cvec);
+    PairTileU<U> ra;
+    issue_pair<DT, ALIGNED, false>(row, nullptr, q0, q1, a.V, ra);
     const float T = a.temperature ? a.temperature[b] : 1.f;
     if (!beam_temperature_ok(T) || !beam_live(a, slot)) return;
-    beam_chunk<DT, ALIGNED>(a, beam_row(a, b, w), slot, chunk, T);
+    const ExpScale e = make_scale(T);
+    BeamRun run = {-INFINITY, -INFINITY, false, 0.0};
+    BeamColumn col = {-INFINITY, -INFINITY, q0};
+    stream_pair<DT, ALIGNED, false>(row, nullptr, q0, q1, a.V, ra, [&](const PairTileU<U> &r, int qb) {
+        col.join(beam_tile<DT, U>(r.t, e, run), -INFINITY, qb);
+    });
+    col.q += tid;
+    const double s = wave_sum(run.s);  // against the wave's maximum
+    // column l of C: threads l, l + C, ...
+    const int C = 1 << a.cols_log;
+    if (a.hinted) {
+        if (C < 64) col.join_lane<32>();
+        if (C < 32) col.join_lane<16>();
+        if (C < 16) col.join_lane<8>();
+        lds_other[tid] = col.other;
+        lds_q[tid] = col.q;
+    } else {
+        if (C < 64) col.best = fmaxf(col.best, lane_xor<32>(col.best));
+        if (C < 32) col.best = fmaxf(col.best, lane_xor<16>(col.best));
+        if (C < 16) col.best = fmaxf(col.best, lane_xor<8>(col.best));
+    }
+    lds_best[tid] = col.best;
+    if (lane == 0) {
+        lds_m[wave] = run.m;
+        lds_s[wave] = s;
+    }
+    __syncthreads();
+    const size_t at = (size_t)slot * a.nc + chunk;
+    if (tid < C) {
+        for (int i = tid + max(C, 64); i < kBlock; i += max(C, 64)) {
+            if (a.hinted) col.join(lds_best[i], lds_other[i], lds_q[i]);
+            else col.best = fmaxf(col.best, lds_best[i]);
+        }
+        a.cols[(at << a.cols_log) + tid] = col.best;
+        if (a.hinted) a.hints[(at << a.cols_log) + tid] = {col.other, col.q};
+    }
+    if (wave != 0) return;
+    const float top = fmaxf(fmaxf(lds_m[0], lds_m[1]), fmaxf(lds_m[2], lds_m[3]));
+    double sum = 0.0;
+    if (lane < kWaves) sum = beam_rebase(lds_s[lane], lds_m[lane], top, e);
+    sum += dpp_double<kDppQuadXor1>(sum);
+    sum += dpp_double<kDppQuadXor2>(sum);
+    if (lane == 0) a.part[at] = {top, 0, sum};
 }
 
 // ---------------------------------------------------------------------------
@@ -444,16 +482,16 @@ struct BeamLoad {
 
 static_assert(2 * kBeamRowChunks <= kMerge, "a thread for each chunk of a sequence, a power of two a row");
 
-template <int DT, bool ALIGNED>
+template <int DT, bool ALIGNED, bool HINTS>
 __global__ __launch_bounds__(kMerge) void beam_merge_kernel(const BeamArgs a)
 {
     __shared__ BeamRow rows[SV_MAX_BEAMS];
     __shared__ float low[SV_MAX_BEAMS];  // no smaller logit of the row reaches the floor
     __shared__ __align__(16) char lds[kBeamSlow * 8];
     __shared__ BeamCand cand[kBeamKeep];
-    __shared__ int hits[kBeamHits];
+    __shared__ int hits[kBeamHits], near[kBeamHits];
     __shared__ float lds_k[kBlock + 1];
-    __shared__ int n_hits, n_cand, errors, lds_i[kMerge / 64];
+    __shared__ int n_hits, n_cand, any_far, errors, lds_i[kMerge / 64];
     const int b = blockIdx.x, tid = threadIdx.x;
     const int n_cols = (a.W * a.nc) << a.cols_log;
     // everything the normalisers and the floor need is requested at once: a
@@ -473,7 +511,7 @@ __global__ __launch_bounds__(kMerge) void beam_merge_kernel(const BeamArgs a)
     BeamPart p = a.part[(size_t)slot * a.nc + min(chunk, a.nc - 1)];
     const bool ended = a.finished && a.finished[slot];
     const float T = a.temperature ? a.temperature[b] : 1.f;
-    if (tid == 0) n_hits = n_cand = errors = 0;
+    if (tid == 0) n_hits = n_cand = any_far = errors = 0;
     __syncthreads();
     const bool good_t = beam_temperature_ok(T);
     const ExpScale e = make_scale(good_t ? T : 1.f);
@@ -537,11 +575,16 @@ __global__ __launch_bounds__(kMerge) void beam_merge_kernel(const BeamArgs a)
             const double m = (double)r.m, d = ((double)tau - r.base) * (double)T;
             return (float)(m + d - 0x1p-20 * (fabs(m) + fabs(d)));
         };
+        auto keep = [&](double c, uint64_t key, int w) {
+            const int at = atomicAdd(&n_cand, 1);
+            if (at < kBeamKeep) cand[at] = {double_order(c), key, w};
+        };
         if (best >= tau) {
             const float least = floor_of(r);
+            if (alone) keep(r.base, top_key(0.f, a.eos), own);
 #pragma unroll
             for (int j = 0; j < kBeamPre; ++j) {
-                if (j >= per || !(alone ? j == 0 : x[j] >= least && x[j] > -INFINITY)) continue;
+                if (alone || j >= per || !(x[j] >= least && x[j] > -INFINITY)) continue;
                 const int at = atomicAdd(&n_hits, 1);
                 if (at < kBeamHits) hits[at] = col0 + j;
             }
@@ -549,31 +592,34 @@ __global__ __launch_bounds__(kMerge) void beam_merge_kernel(const BeamArgs a)
         if (tid < a.W) low[tid] = floor_of(rows[tid]);
         __syncthreads();
         const int nh = n_hits;
-        if (nh <= kBeamHits) {
-            constexpr int VEC = Elt<DT>::kVec;
-            auto keep = [&](double c, uint64_t key, int w) {
-                const int at = atomicAdd(&n_cand, 1);
-                if (at < kBeamKeep) cand[at] = {double_order(c), key, w};
-            };
-            const int C = 1 << a.cols_log, nv = (a.cvec + C - 1) >> a.cols_log;  // vectors per column
-            for (int i0 = tid; i0 < nh * nv; i0 += kBeamAgain * kMerge) {
+        constexpr int VEC = Elt<DT>::kVec;
+        const int C = 1 << a.cols_log;
+        // a long column is read again only at its maximum's tile when its other
+        // tiles stay below the floor, which almost all do
+        const bool hinted = HINTS && nh <= kBeamHits;
+        if (hinted) {
+            if (tid < nh) {
+                const BeamHint h = a.hints[(size_t)b * n_cols + hits[tid]];
+                near[tid] = h.other < low[row_of(hits[tid] >> a.cols_log)] ? h.q : -1;
+                if (near[tid] < 0) any_far = 1;
+            }
+            __syncthreads();
+        }
+        for (int far = hinted ? 0 : 1; far < (hinted && !any_far ? 1 : 2) && nh <= kBeamHits; ++far) {
+            const int each = far ? a.nv : kBeamLoads;
+            for (int i0 = tid; i0 < nh * each; i0 += kBeamAgain * kMerge) {
                 // every load of a batch is unconditional (the maxima stand in
                 // where there is no vector), so that all are in flight at once
                 BeamLoad<DT, ALIGNED> in[kBeamAgain];
                 int q[kBeamAgain], w[kBeamAgain];
 #pragma unroll
                 for (int j = 0; j < kBeamAgain; ++j) {
-                    const int i = i0 + j * kMerge, h = min(i / nv, nh - 1), v = i - h * nv;
-                    const int col = hits[h], chunk = col >> a.cols_log;
+                    const int i = i0 + j * kMerge, h = min(i / each, nh - 1), v = i - h * each;
+                    const int col = hits[h], chunk = col >> a.cols_log, from = hinted ? near[h] : -1;
                     w[j] = row_of(chunk);
                     const int q0 = (chunk - w[j] * a.nc) * a.cvec;
-                    q[j] = q0 + (col & (C - 1)) + (v << a.cols_log);
-                    const bool none = i >= nh * nv || q[j] >= min(a.nvec, q0 + a.cvec);
-                    if (rows[w[j]].state == 2) {
-                        if (!none && v == 0) keep(rows[w[j]].base, top_key(0.f, a.eos), w[j]);
-                        q[j] = -1;
-                    }
-                    if (none) q[j] = -1;
+                    q[j] = far ? q0 + (col & (C - 1)) + (v << a.cols_log) : from + v * kBlock;
+                    if (i >= nh * each || (from < 0) == !far || q[j] >= min(a.nvec, q0 + a.cvec)) q[j] = -1;
                     in[j].issue(q[j] >= 0 ? beam_row(a, b, w[j]) + (size_t)q[j] * 16 : reinterpret_cast<const char *>(cols),
                                q[j] >= 0 ? min(VEC, a.V - q[j] * VEC) : 1);
                 }
@@ -633,10 +679,12 @@ static void launch_beam(const BeamArgs &a, hipStream_t s)
     const unsigned grid = (unsigned)((int64_t)a.B * a.W * a.nc);
     if (a.aligned) {
         beam_rows_kernel<DT, true><<<grid, kBlock, 0, s>>>(a);
-        beam_merge_kernel<DT, true><<<(unsigned)a.B, kMerge, 0, s>>>(a);
+        if (a.hinted) beam_merge_kernel<DT, true, true><<<(unsigned)a.B, kMerge, 0, s>>>(a);
+        else beam_merge_kernel<DT, true, false><<<(unsigned)a.B, kMerge, 0, s>>>(a);
     } else {
         beam_rows_kernel<DT, false><<<grid, kBlock, 0, s>>>(a);
-        beam_merge_kernel<DT, false><<<(unsigned)a.B, kMerge, 0, s>>>(a);
+        if (a.hinted) beam_merge_kernel<DT, false, true><<<(unsigned)a.B, kMerge, 0, s>>>(a);
+        else beam_merge_kernel<DT, false, false><<<(unsigned)a.B, kMerge, 0, s>>>(a);
     }
 }
 
@@ -682,9 +730,12 @@ int32_t spec_beam_select(const void *logits, int32_t B, int32_t W, int32_t V, in
     a.cvec = p.cvec;
     a.cols_log = p.cols_log;
     a.per = p.per;
+    a.nv = (p.cvec + (1 << p.cols_log) - 1) >> p.cols_log;
+    a.hinted = a.nv >= sv::kBeamLong;
     a.g_log = p.g_log;
     a.part = static_cast<sv::BeamPart *>(workspace);
     a.cols = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.off_cols);
+    a.hints = reinterpret_cast<sv::BeamHint *>(static_cast<char *>(workspace) + p.off_hints);
     a.out_score = out_score;
     a.out_parent = out_parent;
     a.out_token = out_token;

@@ -39,8 +39,8 @@ extern "C" {
  *   c(w, v) = s_w + z_w(v) / T - ln sum_u exp(z_w(u) / T)
  * over beams w < W and tokens v < V with z_w(v) > -inf.  A beam with
  * s_w == -inf, or whose logits are all -inf, has no candidate; a finished
- * beam (finished[b, w] != 0) has one, (w, eos) at c = s_w; the logits of
- * neither kind are needed (those of dead and finished beams are not read).
+ * beam (finished[b, w] != 0) has one, (w, eos) at c = s_w.  The logits of dead
+ * and finished beams have no effect, NaN among them.
  * Out come the M candidates of largest c in descending order, equal ones by
  * lower beam, then larger logit, then lower token; where there are fewer, the
  * rest are (-inf, -1, -1).  Order is decided on c in 64 bits, with the sum of
@@ -54,7 +54,7 @@ extern "C" {
  *   out_finished [B, M] int32 or NULL: 1 where the parent was finished or the
  *                token is eos, else 0
  * A sequence with a bad temperature or score, or a NaN or +inf logit in a
- * beam that is read (SV_ERR_ROW), gets -inf, -1, -1 and 0 throughout.
+ * beam in the running (SV_ERR_ROW), gets -inf, -1, -1 and 0 throughout.
  * 1 <= W <= SV_MAX_BEAMS, 1 <= M <= SV_MAX_CANDIDATES, W * V < 2^31.
  * Two kernel launches.  out_score may be scores, and out_finished may be
  * finished, when M == W (the loop's own buffers).

@@ -47,7 +47,8 @@ def check(out, logits, scores, T, M, finished=None, eos=-1):
 
 SIZES = [(1, 1, 1, 1), (1, 1, 7, 4), (2, 3, 50, 6), (1, 2, 3, 64), (3, 4, 1000, 8), (1, 4, 32000, 8),
          (5, 5, 50021, 10), (2, 32, 4099, 64), (300, 2, 513, 4), (1, 1, 200003, 64), (3, 1, 128256, 1),
-         (40, 8, 20011, 16), (1, 16, 65536, 32), (200, 8, 8200, 16)]
+         (40, 8, 20011, 16), (1, 16, 65536, 32), (200, 8, 8200, 16),
+         (8, 8, 128256, 16), (7, 9, 100003, 20)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
@@ -143,6 +144,21 @@ def test_select_ordered_and_tied_rows(sv, kind, V):
     c = beam_candidates(z[0].cpu().numpy(), s[0].cpu().numpy(), 1.0)
     flat = np.lexsort((np.arange(W * V), -c.ravel()))[:M]
     assert np.array_equal(out[1].cpu().numpy()[0], flat // V) and np.array_equal(out[2].cpu().numpy()[0], flat % V)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V,step", [(128256, 1024), (128256, 256), (128256, 1), (100003, 32), (128253, 4096)])
+def test_select_best_tokens_close_together(sv, V, step, dtype):
+    """All the best tokens in 16-byte vectors `step` apart: in one lane's
+    share of the row, in one tile, or side by side."""
+    B, W, M, vec = 8, 8, 16, 4 if dtype == torch.float32 else 8
+    z, s = make(B, W, V, dtype, seed=step)
+    z = z.contiguous()
+    for b in range(B):
+        at = torch.arange(6, device="cuda") * step * vec + 37 * b + b * 8 * vec
+        at = at[at < V]
+        z[b, b % W, at] = (40 - 0.5 * torch.arange(at.numel(), device="cuda")).to(dtype)
+    check(sv.beam_select(z, s, M), z, s, 1.0, M)
 
 
 def test_select_reports_bad_data(sv):
