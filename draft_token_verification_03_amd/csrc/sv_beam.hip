@@ -570,10 +570,13 @@ __global__ __launch_bounds__(kMerge) void beam_merge_kernel(const BeamArgs a)
             best = beam_rough(r.base);
         }
         const float tau = fmaxf(block_kth(best, a.M, lds_k), -FLT_MAX);
-        // the floor as a logit of a row, held low enough for every rounding on the way
+        // the floor as a logit of a row, held low enough for every rounding on
+        // the way: that of the floor itself (half a step of |tau|, in units of T
+        // as a logit), and those of m, the difference and the result
         auto floor_of = [&](const BeamRow &r) {
+            if (tau == -FLT_MAX) return -INFINITY;  // no floor, or one that rounding held up
             const double m = (double)r.m, d = ((double)tau - r.base) * (double)T;
-            return (float)(m + d - 0x1p-20 * (fabs(m) + fabs(d)));
+            return (float)(m + d - 0x1p-20 * (fabs(m) + fabs(d) + fabs((double)tau) * (double)T));
         };
         auto keep = [&](double c, uint64_t key, int w) {
             const int at = atomicAdd(&n_cand, 1);

@@ -285,6 +285,9 @@ class CacheExtend(_Bound):
         self.granted = self._new((B,)) if granted is None else _need("granted", granted, (B,), torch.int32, dev)
         self.error_word = (self._new((1,), zero=True) if error_word is None
                            else _need("error_word", error_word, (1,), torch.int32, dev))
+        if B == 0:  # no sequence: nothing is enqueued that would write them
+            with torch.cuda.stream(self._stream):
+                self.slots.fill_(-1), self.positions.zero_(), self.seq_ids.fill_(-1)
         self._out = (self.slots, self.positions, self.seq_ids, self.query_start, self.granted)
         self._keep = (seq_len, new_len, block_table, free_list, free_count, free_count_out)
         self._fn = lib.spec_cache_extend

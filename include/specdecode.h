@@ -45,7 +45,9 @@ extern "C" {
  * lower beam, then larger logit, then lower token; where there are fewer, the
  * rest are (-inf, -1, -1).  Order is decided on c in 64 bits, with the sum of
  * exponentials in fp32 per 16-byte vector and fp64 beyond (error of the
- * logarithm ~1e-8); out_score is c rounded to fp32.
+ * logarithm ~1e-8); out_score is c rounded to fp32 (to -inf below its range,
+ * as for a token masked by the type's lowest value at T < 1: parent and token
+ * tell such a candidate from none).
  *   logits       element (b, w, v) at b * seq_stride + w * beam_stride + v,
  *                strides >= 0 in elements (0 shares rows), dtype SV_F32/SV_BF16
  *   temperature  [B] float, > 0 and finite (else SV_ERR_TEMPERATURE), or NULL: 1

@@ -53,7 +53,7 @@ def check_beams(c, out_score, out_parent, out_token, M):
     fine = np.isfinite(best32)
     assert np.array_equal(got[~fine], best32[~fine])
     assert np.all(np.abs(got[fine] - best[fine]) <= beam_tolerance(best[fine], V)), (got, best)
-    assert np.all(np.diff(out_score[:n]) <= 0)
+    assert np.all(out_score[1:n] <= out_score[:max(n - 1, 0)])
     assert np.all((out_parent[:n] >= 0) & (out_parent[:n] < W) & (out_token[:n] >= 0) & (out_token[:n] < V))
     at = c[out_parent[:n], out_token[:n]]
     assert np.all(at > -np.inf)

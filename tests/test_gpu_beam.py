@@ -116,6 +116,35 @@ def test_select_masks_of_the_lowest_value(sv, dtype, T):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T", [1.0, 0.25])
+def test_select_reaches_masked_tokens_when_nothing_else_is_left(sv, dtype, T):
+    """Three tokens, the others at the type's lowest value: these follow, at
+    scores that may round to -inf, but with a beam and a token."""
+    V, M = 5000, 12
+    z = torch.full((2, 1, V), torch.finfo(dtype).min, dtype=dtype, device="cuda")
+    z[0, 0, [7, 4000, 4001]] = torch.tensor([1.0, 3.0, 2.0], device="cuda").to(dtype)
+    z[1, 0, 100:] = -float("inf")
+    z[1, 0, 5] = 0.5
+    s = torch.full((2, 1), -1.0, device="cuda")
+    score, parent, token, _, err = sv.beam_select(z, s, M, temperature=T)
+    assert int(err) == 0 and torch.all(parent == 0)
+    assert token[0].tolist() == [4000, 4001, 7, 0, 1, 2, 3, 4, 5, 6, 8, 9]
+    assert token[1].tolist() == [5, 0, 1, 2, 3, 4, 6, 7, 8, 9, 10, 11]
+    check((score, parent, token, torch.zeros_like(parent), err), z, s, T, M)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", [-5e3, -3e6, -1e30])
+@pytest.mark.parametrize("V", [4096, 128256])
+def test_select_scores_of_long_sequences(sv, V, score, dtype):
+    """Scores whose fp32 steps are as large as the candidates' distances."""
+    z, s = make(3, 4, V, dtype, seed=4)
+    s = s * 0 + score
+    s[1, 2:] = score * 1.5
+    check(sv.beam_select(z, s, 16, temperature=1.5), z, s, 1.5, 16)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("B,W,V,M", [(1, 1, 40000, 16), (2, 4, 128256, 8), (1, 3, 300, 64), (3, 2, 9001, 64)])
 def test_select_ties_go_to_the_lowest_index(sv, B, W, V, M, dtype):
     """Equal logits and scores everywhere: tokens 0, 1, ... of beam 0."""
