@@ -42,7 +42,12 @@ constexpr int kBeamHits = 256;       // columns read again
 constexpr int kBeamLong = 40;        // vectors from which on a column is read again by its hint
 constexpr int kBeamKeep = 512;       // candidates ranked at once
 constexpr int kBeamRound = 256;      // vectors the slow path takes at once
-constexpr int kBeamSlow = kBeamRound * 8 + SV_MAX_CANDIDATES;  // their keys and the best so far
+constexpr int kBeamCut = 704;        // keys its cuts leave at most: of kBeamSlow, 11 from each of 64 threads
+constexpr int kBeamSlow = kBeamRound * 8 + kBeamCut;
+static_assert((kBeamSlow + kBlock - 1) / kBlock * SV_MAX_CANDIDATES <= kBeamCut, "a cut leaves M threads' keys");
+constexpr int kBeamRowKeep = 192;    // keys a row's last cut leaves: of kBeamCut, 3 from each of 64 threads
+static_assert((kBeamCut + kBlock - 1) / kBlock * SV_MAX_CANDIDATES <= kBeamRowKeep &&
+                  kBeamRowKeep + SV_MAX_CANDIDATES <= kBeamKeep, "a row's keys and the best so far");
 
 struct BeamPart {
     float m;     // chunk maximum
@@ -344,48 +349,38 @@ __device__ __forceinline__ uint4 beam_vector(const BeamArgs &a, const char *row,
 
 // ---------------------------------------------------------------------------
 // When more candidates reach the floor than are ranked at once (many equal
-// ones), row by row: the best M keys of a row, vectors in index order, kBeamRound
-// at a time, those that beat the best M so far collected and cut back to
-// M.  A row ends early when its M-th best logit equals its maximum: whatever
-// follows has a larger index.
+// ones, or the best all in neighbouring columns), row by row: vectors in index
+// order, kBeamRound at a time, those keys collected that beat a floor under the
+// row's M-th best so far.  A row ends early when that floor's logit is the
+// row's maximum: whatever follows has a larger index.  (64 x 8 x 152064 bf16:
+// all logits equal 0.1 ms, a cut at many equal ones below the best 0.7 ms.)
 
-// The best M of buf[0, n), n >= M, moved to its front (unordered): the M-th
-// largest key by its bits from the top, counting.
-__device__ __forceinline__ uint64_t beam_cut(uint64_t *buf, int n, int M, int *cnt, int *ldsi)
+// Raises the floor: the M-th largest of 256 threads' largest keys, which
+// leaves the keys of M threads in buf[0, n); returns how many.
+__device__ __forceinline__ int beam_cut(uint64_t *buf, int n, int M, uint64_t &floor, int *cnt, uint64_t *lds_k)
 {
-    uint64_t kth = 0;
-    for (int bit = 63; bit >= 0; --bit) {
-        const uint64_t c = kth | (1ull << bit);
-        int k = 0;
-        for (int i = threadIdx.x; i < n; i += kMerge) k += buf[i] >= c;
-        k = wave_sum_int(k);
-        if ((threadIdx.x & 63) == 0) ldsi[threadIdx.x >> 6] = k;
-        __syncthreads();
-        k = 0;
-        for (int i = 0; i < kMerge / 64; ++i) k += ldsi[i];
-        __syncthreads();
-        if (k >= M) kth = c;
-    }
-    // keys are distinct: M of them are >= kth
-    constexpr int kOwn = (kBeamSlow + kMerge - 1) / kMerge;
-    uint64_t own[kOwn];
+    constexpr int kOwn = (kBeamSlow + kBlock - 1) / kBlock;
+    uint64_t own[kOwn], best = 0;
 #pragma unroll
     for (int j = 0; j < kOwn; ++j) {
-        const int i = threadIdx.x + j * kMerge;
-        own[j] = i < n ? buf[i] : 0;
+        const int i = threadIdx.x + j * kBlock;
+        own[j] = (int)threadIdx.x < kBlock && i < n ? buf[i] : 0;
+        best = larger(best, own[j]);
     }
     if (threadIdx.x == 0) *cnt = 0;
-    __syncthreads();
+    floor = larger(floor, block_kth(best, M, lds_k));
 #pragma unroll
     for (int j = 0; j < kOwn; ++j)
-        if (own[j] >= kth) buf[atomicAdd(cnt, 1)] = own[j];
+        if (own[j] && own[j] >= floor) buf[atomicAdd(cnt, 1)] = own[j];
     __syncthreads();
-    return kth;
+    n = *cnt;
+    __syncthreads();
+    return n;
 }
 
 template <int DT>
 __device__ __forceinline__ int beam_row_slow(const BeamArgs &a, const BeamRow &r, const char *row, float floor_c,
-                                          double inv_t, uint64_t *buf, int *cnt, int *ldsi)
+                                          double inv_t, uint64_t *buf, int *cnt, uint64_t *lds_k)
 {
     constexpr int VEC = Elt<DT>::kVec;
     uint64_t floor = 0;
@@ -407,28 +402,28 @@ __device__ __forceinline__ int beam_row_slow(const BeamArgs &a, const BeamRow &r
         __syncthreads();
         n = *cnt;
         __syncthreads();
-        if (n > SV_MAX_CANDIDATES) {
-            floor = beam_cut(buf, n, a.M, cnt, ldsi);
-            n = a.M;
+        if (n > kBeamCut) {
+            n = beam_cut(buf, n, a.M, floor, cnt, lds_k);
             if (key_value(floor) == r.m) break;
         }
     }
+    while (n > kBeamRowKeep) n = beam_cut(buf, n, a.M, floor, cnt, lds_k);
     return n;
 }
 
 // The best M into cand[0, n) in order; returns n.
 template <int DT>
 __device__ __forceinline__ int beam_slow(const BeamArgs &a, const BeamRow *rows, int b, float floor_c, double inv_t,
-                                      BeamCand *cand, uint64_t *buf, int *cnt, int *ldsi)
+                                      BeamCand *cand, uint64_t *buf, int *cnt, uint64_t *lds_k)
 {
     int n = 0;
     for (int w = 0; w < a.W; ++w) {
         const BeamRow r = rows[w];
-        if (r.state == 0) continue;
-        const double top = r.base;  // of its best, c at z = m
-        if (n == a.M && double_order(top) <= cand[n - 1].c) continue;  // a later beam loses a tie
+        // base is c of the row's best; a later beam loses a tie
+        if (r.state == 0 || beam_rough(r.base) < floor_c || (n == a.M && double_order(r.base) <= cand[n - 1].c))
+            continue;
         int k = 1;
-        if (r.state == 1) k = beam_row_slow<DT>(a, r, beam_row(a, b, w), floor_c, inv_t, buf, cnt, ldsi);
+        if (r.state == 1) k = beam_row_slow<DT>(a, r, beam_row(a, b, w), floor_c, inv_t, buf, cnt, lds_k);
         __syncthreads();
         for (int i = threadIdx.x; i < k; i += kMerge) {
             const uint64_t key = r.state == 2 ? top_key(0.f, a.eos) : buf[i];
@@ -450,7 +445,6 @@ __device__ __forceinline__ int beam_slow(const BeamArgs &a, const BeamRow *rows,
     }
     return n;
 }
-static_assert(2 * SV_MAX_CANDIDATES <= kMerge, "a row's best beside the best so far, one per thread");
 
 // A 16-byte vector requested now and put together later: of an unaligned
 // address the two aligned blocks that hold its `valid` elements (the first
@@ -490,8 +484,8 @@ __global__ __launch_bounds__(kMerge) void beam_merge_kernel(const BeamArgs a)
     __shared__ __align__(16) char lds[kBeamSlow * 8];
     __shared__ BeamCand cand[kBeamKeep];
     __shared__ int hits[kBeamHits], near[kBeamHits];
-    __shared__ float lds_k[kBlock + 1];
-    __shared__ int n_hits, n_cand, any_far, errors, lds_i[kMerge / 64];
+    __shared__ uint64_t lds_k[kBlock + 1];
+    __shared__ int n_hits, n_cand, any_far, errors;
     const int b = blockIdx.x, tid = threadIdx.x;
     const int n_cols = (a.W * a.nc) << a.cols_log;
     // everything the normalisers and the floor need is requested at once: a
@@ -569,7 +563,8 @@ __global__ __launch_bounds__(kMerge) void beam_merge_kernel(const BeamArgs a)
         } else if (mine && alone) {
             best = beam_rough(r.base);
         }
-        const float tau = fmaxf(block_kth(best, a.M, lds_k), -FLT_MAX);
+        float *lds_f = reinterpret_cast<float *>(lds_k);
+        const float tau = fmaxf(block_kth(best, a.M, lds_f), -FLT_MAX);
         // the floor as a logit of a row, held low enough for every rounding on
         // the way: that of the floor itself (half a step of |tau|, in units of T
         // as a logit), and those of m, the difference and the result
@@ -582,6 +577,8 @@ __global__ __launch_bounds__(kMerge) void beam_merge_kernel(const BeamArgs a)
             const int at = atomicAdd(&n_cand, 1);
             if (at < kBeamKeep) cand[at] = {double_order(c), key, w};
         };
+        constexpr int VEC = Elt<DT>::kVec;
+        const int C = 1 << a.cols_log;
         if (best >= tau) {
             const float least = floor_of(r);
             if (alone) keep(r.base, top_key(0.f, a.eos), own);
@@ -594,13 +591,10 @@ __global__ __launch_bounds__(kMerge) void beam_merge_kernel(const BeamArgs a)
         }
         if (tid < a.W) low[tid] = floor_of(rows[tid]);
         __syncthreads();
-        const int nh = n_hits;
-        constexpr int VEC = Elt<DT>::kVec;
-        const int C = 1 << a.cols_log;
+        const int nh = min(n_hits, kBeamHits);
         // a long column is read again only at its maximum's tile when its other
         // tiles stay below the floor, which almost all do
-        const bool hinted = HINTS && nh <= kBeamHits;
-        if (hinted) {
+        if (HINTS) {
             if (tid < nh) {
                 const BeamHint h = a.hints[(size_t)b * n_cols + hits[tid]];
                 near[tid] = h.other < low[row_of(hits[tid] >> a.cols_log)] ? h.q : -1;
@@ -608,7 +602,7 @@ __global__ __launch_bounds__(kMerge) void beam_merge_kernel(const BeamArgs a)
             }
             __syncthreads();
         }
-        for (int far = hinted ? 0 : 1; far < (hinted && !any_far ? 1 : 2) && nh <= kBeamHits; ++far) {
+        for (int far = HINTS ? 0 : 1; far < (HINTS && !any_far ? 1 : 2); ++far) {
             const int each = far ? a.nv : kBeamLoads;
             for (int i0 = tid; i0 < nh * each; i0 += kBeamAgain * kMerge) {
                 // every load of a batch is unconditional (the maxima stand in
@@ -618,13 +612,14 @@ __global__ __launch_bounds__(kMerge) void beam_merge_kernel(const BeamArgs a)
 #pragma unroll
                 for (int j = 0; j < kBeamAgain; ++j) {
                     const int i = i0 + j * kMerge, h = min(i / each, nh - 1), v = i - h * each;
-                    const int col = hits[h], chunk = col >> a.cols_log, from = hinted ? near[h] : -1;
+                    const int col = hits[h], chunk = col >> a.cols_log, from = HINTS ? near[h] : -1;
                     w[j] = row_of(chunk);
                     const int q0 = (chunk - w[j] * a.nc) * a.cvec;
                     q[j] = far ? q0 + (col & (C - 1)) + (v << a.cols_log) : from + v * kBlock;
                     if (i >= nh * each || (from < 0) == !far || q[j] >= min(a.nvec, q0 + a.cvec)) q[j] = -1;
-                    in[j].issue(q[j] >= 0 ? beam_row(a, b, w[j]) + (size_t)q[j] * 16 : reinterpret_cast<const char *>(cols),
-                               q[j] >= 0 ? min(VEC, a.V - q[j] * VEC) : 1);
+                    const bool some = q[j] >= 0;
+                    in[j].issue(some ? beam_row(a, b, w[j]) + (size_t)q[j] * 16 : reinterpret_cast<const char *>(cols),
+                                some ? min(VEC, a.V - q[j] * VEC) : 1);
                 }
 #pragma unroll
                 for (int j = 0; j < kBeamAgain; ++j) {
@@ -635,21 +630,24 @@ __global__ __launch_bounds__(kMerge) void beam_merge_kernel(const BeamArgs a)
                     const float least = low[w[j]];
                     uint32_t at = 0;  // elements that may reach the floor
 #pragma unroll
-                    for (int k = 0; k < VEC; ++k)
-                        at |= (z[k] >= least && z[k] != -INFINITY && q[j] * VEC + k < a.V) ? 1u << k : 0u;
+                    for (int e = 0; e < VEC; ++e)
+                        at |= (z[e] >= least && z[e] != -INFINITY && q[j] * VEC + e < a.V) ? 1u << e : 0u;
+                    // (no more once there are too many)
+                    if (at && *const_cast<volatile int *>(&n_cand) > kBeamKeep) at = 0;
                     for (; at; at &= at - 1) {
-                        const int k = __ffs(at) - 1;
-                        const float zk = elt_of<DT>(vec, k);
-                        const double c = beam_c(rows[w[j]], zk, inv_t);
-                        if (beam_rough(c) >= tau) keep(c, top_key(zk, q[j] * VEC + k), w[j]);
+                        const int e = __ffs(at) - 1;
+                        const float ze = elt_of<DT>(vec, e);
+                        const double c = beam_c(rows[w[j]], ze, inv_t);
+                        if (beam_rough(c) >= tau) keep(c, top_key(ze, q[j] * VEC + e), w[j]);
                     }
                 }
             }
         }
         __syncthreads();
         const int k = n_cand;
+        const bool whole = n_hits <= kBeamHits && k <= kBeamKeep;
         __syncthreads();  // the slow path counts with n_cand too
-        if (nh <= kBeamHits && k <= kBeamKeep) {
+        if (whole) {
             // distinct candidates: a place is the number of better ones
             // (eight lanes to a candidate)
             for (int i0 = 0; i0 < k; i0 += kMerge / 8) {
@@ -664,7 +662,13 @@ __global__ __launch_bounds__(kMerge) void beam_merge_kernel(const BeamArgs a)
             }
             found = min(k, a.M);
         } else {
-            found = beam_slow<DT>(a, rows, b, tau, inv_t, cand, reinterpret_cast<uint64_t *>(lds), &n_cand, lds_i);
+            // the candidates found so far may give a higher floor
+            float mine = -INFINITY;
+            if (tid < kBlock)
+                for (int i = tid; i < min(k, kBeamKeep); i += kBlock)
+                    mine = fmaxf(mine, beam_rough(order_double(cand[i].c)));
+            const float floor_c = fmaxf(tau, block_kth(mine, a.M, lds_f));
+            found = beam_slow<DT>(a, rows, b, floor_c, inv_t, cand, reinterpret_cast<uint64_t *>(lds), &n_cand, lds_k);
             for (int i = tid; i < found; i += kMerge) put(i, cand[i]);
         }
     }
