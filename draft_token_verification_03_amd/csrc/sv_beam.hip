@@ -32,14 +32,19 @@ namespace sv {
 
 constexpr double kLn2 = 0.6931471805599453;
 constexpr int kBeamLoads = 4;        // 16-byte vectors per thread per tile
-constexpr int kBeamFill = 512;       // workgroups the streaming grid aims for: two per CU
+// Workgroups the streaming grid aims for: two per CU.  (32 x 8 x 128256 bf16
+// 23.3 us, with 768 24.9, with 1536 24.6; no difference beyond 1 us elsewhere.)
+constexpr int kBeamFill = 512;
 constexpr int kBeamMaxChunks = 64;   // chunks per row: the merge gives each a lane
 constexpr int kBeamRowChunks = 256;  // W * chunks at most: with lanes to spare, one thread each in the merge
 constexpr int kBeamPre = 8;          // column maxima per thread of the merge
 constexpr int kMerge = 1024;         // threads of the merge: 256 hold columns, all of them read columns again
 constexpr int kBeamAgain = 2;        // vectors each requests at once
 constexpr int kBeamHits = 256;       // columns read again
-constexpr int kBeamLong = 40;        // vectors from which on a column is read again by its hint
+// Vectors from which on a column is read again by its hint, which costs a
+// round trip: at 63 vectors a column 22.1 us with and 23.7 without (32 x 8 x
+// 128256 bf16), at 32 12.5 with and 12.1 without (4 x 4 x 128256 bf16).
+constexpr int kBeamLong = 40;
 constexpr int kBeamKeep = 512;       // candidates ranked at once
 constexpr int kBeamRound = 256;      // vectors the slow path takes at once
 constexpr int kBeamCut = 704;        // keys its cuts leave at most: of kBeamSlow, 11 from each of 64 threads
@@ -218,6 +223,9 @@ __device__ __forceinline__ bool beam_live(const BeamArgs &a, int slot)
 
 // The first tile is requested before the beam's score and temperature are
 // known, so the stream starts a round trip earlier; a dead beam wastes it.
+// Bound by reading: 27 us for 156 MB of bf16 (64 x 8 x 152064, 5.8 TB/s), 41 us
+// for 263 MB of fp32 (128 x 4 x 128256, 6.4 TB/s), 3 to 4 us for one request.
+// Lists kept while streaming (an earlier form) took 47 us for the former.
 template <int DT, bool ALIGNED>
 __global__ __launch_bounds__(kBlock) void beam_rows_kernel(const BeamArgs a)
 {
@@ -474,6 +482,13 @@ struct BeamLoad {
     }
 };
 
+// The merge is a chain of memory round trips (inputs, columns read again) and
+// barriers, 7 to 10 us, hardly depending on the sizes: 1.3 us until the inputs
+// are there, 1.3 the normalisers in fp64, 0.9 the floor's sorts, 0.8 the
+// columns that reach it, 1.2 to 1.8 reading them again, 0.6 the ranks.  Its
+// code is kept short, each step once, since a step runs once per call and
+// fetching its instructions counts (checks unrolled over 64 elements took 4
+// us more).
 static_assert(2 * kBeamRowChunks <= kMerge, "a thread for each chunk of a sequence, a power of two a row");
 
 template <int DT, bool ALIGNED, bool HINTS>

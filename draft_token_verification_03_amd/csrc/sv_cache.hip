@@ -11,7 +11,11 @@
 // step is dependent memory round trips: lengths, then pages.  Up to kPlan
 // sequences have a thread each, their sums stay in LDS, and then every
 // sequence gets as many lanes as there are to spare for its tokens, so that
-// nothing searches and no trip is added.
+// nothing searches and no trip is added.  64 sequences: extend by 6 tokens
+// 3.7 us of kernel, commit 2.5 us, where an empty launch takes 3.5 us from one
+// to the next; 256 sequences with up to 4096 new tokens each 4.4 us for the
+// scan and 9.5 us for a million tokens' places; the end of a step of 2000
+// sequences, 100 of them giving all their pages back, 5.0 and 5.1 us.
 #include <algorithm>
 
 #include "specdecode.h"
@@ -21,8 +25,14 @@ namespace sv {
 
 constexpr int kPlan = 1024;             // threads of the scanning workgroup
 constexpr int kPlanWaves = kPlan / 64;
-constexpr int kFusedTokens = 8192;      // at most so many tokens in the scanning workgroup
-constexpr int kFusedPages = 65536;      // the same for pages that can come back
+// At most so many tokens are placed by the scanning workgroup (64 sequences:
+// 384 tokens 4.7 us, with a launch of their own 7.5; 4096 8.0 and 9.7; 8192 9.6
+// and 9.9; 512 sequences, 8192 tokens 17.8 and 11.9).
+constexpr int kFusedTokens = 4096;
+// The same for pages that could come back when sequences end, which few do in
+// a step (64 sequences of up to 512 blocks: none ends 4.3 us, with a launch of
+// their own 7.1; a tenth 5.3 to 8.7 and 7.2; all of them 34 and 7.2).
+constexpr int kFusedPages = 65536;
 constexpr int kMaxCacheSeqs = 1 << 20;
 
 struct CacheArgs {
@@ -94,8 +104,8 @@ __device__ __forceinline__ int free_pages(const CacheArgs &a)
     return held;
 }
 
-constexpr int kTokens = 4;    // per thread where they have a launch of their own
-constexpr int kStaged = 2048;  // sequences whose numbers a workgroup of it copies to LDS
+constexpr int kTokens = 4;    // per thread where they have a launch of their own (1, 2, 8: 15.2, 13.9, 16.7 us against 13.7)
+constexpr int kStaged = 2048;  // sequences whose numbers a workgroup of it copies to LDS (64: 9.9 us against 11.0)
 
 // The last i in [lo, hi) with start[i] <= t (start[lo] <= t).
 __device__ __forceinline__ int find_run(const int32_t *start, int lo, int hi, int t)
@@ -329,16 +339,19 @@ __device__ __forceinline__ Kept kept_tokens(const CacheArgs &a, int b, bool &bad
     return k;
 }
 
-// Page `block` of sequence b, number i of the `total` that come back; the
-// list held `free` before.
-__device__ __forceinline__ void give_page(const CacheArgs &a, int b, int block, int i, int total, int free)
+// Number i of the `total` pages that come back; the list held `free` before.
+__device__ __forceinline__ void put_page(const CacheArgs &a, int page, int i, int total, int free)
 {
-    int page = a.table[(int64_t)b * a.max_blocks + block];
     if (page < 0 || page >= a.num_pages) {
         cache_error(a, SV_ERR_PAGE);
         page = -1;
     }
     a.free_list[free + total - 1 - i] = page;
+}
+
+__device__ __forceinline__ void give_page(const CacheArgs &a, int b, int block, int i, int total, int free)
+{
+    put_page(a, a.table[(int64_t)b * a.max_blocks + block], i, total, free);
 }
 
 // As extend_plan_kernel; FUSED (one round of sequences): their pages too.
@@ -351,7 +364,7 @@ __global__ __launch_bounds__(kPlan) void commit_plan_kernel(const CacheArgs a)
     Kept k = {0, 0, 0};
     bool bad = false;
     if (tid < a.B) k = kept_tokens(a, tid, bad);
-    const int free = free_pages(a), room = a.num_pages - free;
+    const int free = free_pages(a), room = a.num_pages - free, most = k.back;
     int64_t p0 = 0;
     for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
         const int b = b0 + tid;
@@ -377,9 +390,30 @@ __global__ __launch_bounds__(kPlan) void commit_plan_kernel(const CacheArgs a)
         *a.free_count_out = free + total;
     }
     if (!FUSED) return;
-    __syncthreads();
     int lanes = 1;  // per sequence
     while (2 * lanes * a.B <= (int)blockDim.x) lanes *= 2;
+    // a sequence that gives back many pages (its end, usually) has everyone at
+    // work on all of them, each searching for its own
+    if (__syncthreads_or(most > 4 * lanes)) {
+        constexpr int kAtOnce = 4;
+        for (int i0 = tid; i0 < total; i0 += kAtOnce * blockDim.x) {
+            int lo[kAtOnce] = {};
+            for (int step = 1 << (31 - __clz(a.B)); step; step >>= 1)
+#pragma unroll
+                for (int j = 0; j < kAtOnce; ++j)
+                    if (lo[j] + step < a.B && seqs[lo[j] + step].z <= i0 + j * (int)blockDim.x) lo[j] += step;
+            int page[kAtOnce];
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                const int i = min(i0 + j * (int)blockDim.x, total - 1), block = seqs[lo[j]].x + i - seqs[lo[j]].z;
+                page[j] = a.table[(int64_t)lo[j] * a.max_blocks + block];
+            }
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j)
+                if (i0 + j * (int)blockDim.x < total) put_page(a, page[j], i0 + j * (int)blockDim.x, total, free);
+        }
+        return;
+    }
     const int b = tid / lanes;
     if (b < a.B) {
         const int4 v = seqs[b];

@@ -3,7 +3,12 @@
 // tree.  Copies bound by memory, done in place without a second buffer: one
 // thread owns one vector column of all rows that exchange contents, so it
 // has read every source before it writes, and no two threads touch the same
-// bytes.
+// bytes.  Each source that another beam takes over is read once, each beam
+// with another parent written once; nontemporal, since a cache is larger than
+// L2 and read next by other kernels (165 -> 151 us for 0.7 GB).  With every
+// beam moving, bf16: dense W = 4 5.9 TB/s, 8 5.8, 16 5.3, 32 4.9; paged 5.6,
+// 5.5, 5.5, 3.9 (at 32 the columns in registers leave two waves per SIMD); a
+// plain copy of this card's memory runs at 5.1 TB/s.
 #include <algorithm>
 
 #include "specdecode.h"
@@ -58,6 +63,8 @@ __device__ __forceinline__ BeamMoves<WM> beam_moves(const MoveArgs &a, int b)
     return m;
 }
 
+// NV vectors of each beam per thread, so that W NV are in flight: with W = 4
+// 2, 4 and 8 of them take 364, 365 and 381 us for 1.07 GB moved.
 template <class T, int WM, int NV>
 __global__ __launch_bounds__(kBlock) void reorder_dense_kernel(const MoveArgs a)
 {
@@ -171,7 +178,10 @@ constexpr int kPathAhead = 8;  // rows read before the first of them is written
 
 // A workgroup takes kBlock vectors of one position of one sequence, of all
 // pools behind each other.  Its first threads turn the path into row offsets
-// (one round trip for the path, one for the tables), the rest is copies.
+// (one round trip for the path, one for the tables), the rest is copies: 8.5
+// us for 34 MB (64 sequences, 32 pools of 2 KB rows), against 16.6 with the
+// offsets formed by every thread and a workgroup per pool; 4.7 us for four
+// sequences, a launch's time.
 template <class T>
 __global__ __launch_bounds__(kBlock) void compact_kernel(const MoveArgs a)
 {

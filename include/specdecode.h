@@ -129,7 +129,7 @@ int32_t spec_beam_reorder_paged(void *const *pools, int32_t n_pools, int32_t B, 
  * is to be filled, sets SV_ERR_PAGE, and its tokens' slots are -1.
  * seq_len is left as it is: spec_cache_commit says what was kept.
  *   free_list [num_pages] int32;  free_count [1] in [0, num_pages]
- * B <= 2^20.  One kernel launch, two for more than 8192 tokens or 1024 sequences.
+ * B <= 2^20.  One kernel launch, two for more than 4096 tokens or 1024 sequences.
  */
 int32_t spec_cache_extend(const int32_t *seq_len, const int32_t *new_len, int32_t extra, int32_t B,
                           int32_t *block_table, int32_t max_blocks, int32_t page_size, const int32_t *free_list,
