@@ -12,7 +12,7 @@
 // sequences have a thread each, their sums stay in LDS, and then every
 // sequence gets as many lanes as there are to spare for its tokens, so that
 // nothing searches and no trip is added.  64 sequences: extend by 6 tokens
-// 3.7 us of kernel, commit 2.5 us, where an empty launch takes 3.5 us from one
+// 3.7 us of kernel, commit 2.9 us, where an empty launch takes 3.5 us from one
 // to the next; 256 sequences with up to 4096 new tokens each 4.4 us for the
 // scan and 9.5 us for a million tokens' places; the end of a step of 2000
 // sequences, 100 of them giving all their pages back, 5.0 and 5.1 us.
