@@ -53,6 +53,13 @@ def _need(name: str, t, shape, dtype=torch.int32, device=None) -> torch.Tensor:
     return t
 
 
+def _overlap(x: torch.Tensor, y: torch.Tensor) -> bool:
+    """Whether two contiguous tensors share memory."""
+    x0, y0 = x.data_ptr(), y.data_ptr()
+    return (x0 < y0 + y.numel() * y.element_size() and y0 < x0 + x.numel() * x.element_size()
+            and x.numel() > 0 and y.numel() > 0)
+
+
 def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
@@ -140,8 +147,8 @@ class BeamSelector(_Bound):
                                     ("out_tokens", out_tokens, torch.int32, None),
                                     ("out_finished", out_finished, torch.int32, finished)):
             t = self._new((B, M), dtype) if t is None else _need(name, t, (B, M), dtype, dev)
-            if M != W and own is not None and t.data_ptr() == own.data_ptr():
-                raise ValueError(f"{name} can be the call's input only when M == W")
+            if own is not None and _overlap(t, own) and not (M == W and t.data_ptr() == own.data_ptr()):
+                raise ValueError(f"{name} can share memory with the call's input only as that input, when M == W")
             out.append(t)
         self.error_word = self._new((1,), zero=True)
         self._out = (*out, self.error_word)

@@ -386,3 +386,124 @@ def test_reorder_captured(sv):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(x, want)
+
+
+def test_beam_search_loop(sv):
+    """A whole search as a loop runs it: selection into the loop's own buffers,
+    then the beams' states (each beam's tokens so far, in a dense cache and
+    through block tables) to their new places.  The model's logits depend on
+    the beam's last two tokens, so a state in the wrong place goes on wrongly."""
+    B, W, V, steps, eos, page = 3, 4, 211, 9, 5, 4
+    g = torch.Generator().manual_seed(8)
+    table = 2.5 * torch.randn((V, V), generator=g)
+    other = 1.5 * torch.randn((V, V), generator=g)
+    first = torch.randint(6, V, (B,), generator=g)
+
+    def logits_of(last, before):  # [...] -> [..., V]
+        return table[last] + other[before]
+
+    # a plain search, request by request, in 64 bits
+    want = []
+    for b in range(B):
+        beams = [([int(first[b])] * 2, 0.0, False)] + [([int(first[b])] * 2, -np.inf, False)] * (W - 1)
+        for _ in range(steps):
+            z = torch.stack([logits_of(t[-1], t[-2]) for t, _, _ in beams]).numpy()
+            c = beam_candidates(z, [s for _, s, _ in beams], 1.0, [f for _, _, f in beams], eos)
+            order = np.lexsort((np.arange(W * V), -c.ravel()))[:W]
+            beams = [(beams[i // V][0] + [int(i % V)], c.ravel()[i], beams[i // V][2] or i % V == eos) for i in order]
+        want.append(beams)
+
+    dev = "cuda"
+    dense = torch.zeros(B * W, 1, steps + 2, 8, device=dev)
+    blocks = -(-(steps + 2) // page)
+    tab = torch.randperm(B * W * blocks, generator=g).view(B * W, blocks).to(torch.int32).to(dev)
+    paged_ = torch.zeros(B * W * blocks, 1, page, 8, device=dev)
+
+    def at(t):  # rows of position t in the paged cache
+        return paged_.view(-1, 8)[(tab[:, t // page].long() * page + t % page)]
+
+    for t in range(2):
+        dense[:, 0, t] = first.to(dev).repeat_interleave(W)[:, None].float()
+        paged_.view(-1, 8)[tab[:, t // page].long() * page + t % page] = dense[:, 0, t]
+    scores = torch.full((B, W), -float("inf"), device=dev)
+    scores[:, 0] = 0.0
+    fin = torch.zeros((B, W), dtype=torch.int32, device=dev)
+    logits = torch.zeros((B, W, V), device=dev)
+    length = torch.full((B,), 2, dtype=torch.int32, device=dev)
+    parent = torch.zeros((B, W), dtype=torch.int32, device=dev)
+    select = sv.BeamSelector(logits, scores, W, finished=fin, eos=eos, out_scores=scores, out_finished=fin, out_parent=parent)
+    move = sv.BeamReorder(dense, parent, length=length)
+    move_paged = sv.BeamReorder(paged_, parent, length=length, block_table=tab)
+    table, other = table.to(dev), other.to(dev)
+    for t in range(2, steps + 2):
+        last, before = dense[:, 0, t - 1, 0].long(), dense[:, 0, t - 2, 0].long()
+        assert torch.equal(at(t - 1)[:, 0].long(), last)
+        logits.copy_(logits_of(last, before).view(B, W, V))
+        tokens = select()[2]
+        move()
+        move_paged()
+        dense[:, 0, t] = tokens.view(-1, 1).float()
+        paged_.view(-1, 8)[tab[:, t // page].long() * page + t % page] = dense[:, 0, t]
+        length += 1
+    for w in (select, move, move_paged):
+        assert int(w.error_word) == 0
+    for b in range(B):
+        for j in range(W):
+            tokens, score, ended = want[b][j]
+            assert dense[b * W + j, 0, :, 0].long().tolist() == tokens
+            assert bool(fin[b, j]) == bool(ended)
+            assert abs(float(scores[b, j]) - score) <= steps * (abs(score) + 2 * np.log(V) + 5) * 2.0 ** -24
+
+
+def test_empty_batches(sv):
+    z, s = make(1, 3, 50, torch.float32)
+    out = sv.beam_select(z[:0], s[:0], 4)
+    assert all(x.shape == (0, 4) for x in out[:4]) and int(out[4]) == 0
+    none = torch.zeros((0, 3), dtype=torch.int32, device="cuda")
+    sv.beam_reorder(torch.zeros(0, 1, 4, 8, device="cuda"), none)
+    sv.beam_reorder(torch.zeros(6, 1, 0, 8, device="cuda"), torch.zeros((2, 3), dtype=torch.int32, device="cuda"))
+
+
+def test_select_rows_beyond_32_bit_offsets(sv):
+    """1.2e9 tokens a row: the second row starts past 2^31 bytes.  The best
+    tokens are planted, at both ends and between; the others are equal."""
+    V, M = 1_200_000_003, 6
+    z = torch.zeros((2, 1, V), dtype=torch.bfloat16, device="cuda")
+    at = [[V - 1, 0, 1 << 30, 77, V - 9], [5, V - 2, (1 << 30) + 1, 600_000_000, V - 100_000]]
+    vals = [9.0, 8.0, 7.0, 6.0, 5.0]
+    for b in range(2):
+        for i, v in zip(at[b], vals):
+            z[b, 0, i] = v
+    s = torch.zeros((2, 1), device="cuda")
+    score, parent, token, _, err = sv.beam_select(z, s, M)
+    assert int(err) == 0 and torch.all(parent == 0)
+    assert token.tolist() == [at[0] + [1], at[1] + [0]]
+    lse = np.log(V - 5 + sum(np.exp(vals)))
+    assert np.allclose(score.cpu().numpy(), np.array([vals + [0.0]] * 2) - lse, rtol=0, atol=(40 + 2 * np.log(V) + 5) * 2.0 ** -24)
+
+
+def test_reorder_beyond_32_bit_offsets(sv):
+    x = torch.zeros((5, 1, 1 << 19, 1 << 11), dtype=torch.uint8, device="cuda")  # 1 GiB a beam
+    mark = torch.arange(1 << 19, device="cuda")
+    for w in range(5):
+        x[w, 0, :, 0] = (mark * (w + 3) % 251).to(torch.uint8)
+        x[w, 0, :, -1] = (mark * (w + 5) % 241).to(torch.uint8)
+    parent = [2, 0, 4, 3, 0]
+    sv.beam_reorder(x, torch.tensor([parent], dtype=torch.int32, device="cuda"))
+    for w, p in enumerate(parent):
+        assert torch.equal(x[w, 0, :, 0], (mark * (p + 3) % 251).to(torch.uint8))
+        assert torch.equal(x[w, 0, :, -1], (mark * (p + 5) % 241).to(torch.uint8))
+    # the same memory as pages of 2 MiB
+    pages = x.view(5 << 9, 1, 1 << 10, 1 << 11)
+    last = (5 << 9) - 1
+    table = torch.tensor([[last, 0], [1, last - 1]], dtype=torch.int32, device="cuda")
+    old = pages[table.view(-1).long()].clone()
+    sv.beam_reorder(pages, torch.tensor([[1, 0]], dtype=torch.int32, device="cuda"), block_table=table,
+                    length=torch.tensor([2 << 10], dtype=torch.int32, device="cuda"))
+    assert torch.equal(pages[table.view(-1).long()], old[[2, 3, 0, 1]])
+    r = sv.CacheCompact(pages, table[:1], torch.tensor([500], dtype=torch.int32, device="cuda"),
+                        torch.tensor([[2, -1, -1]], dtype=torch.int32, device="cuda"),
+                        torch.tensor([1], dtype=torch.int32, device="cuda"))
+    row = pages[last, 0, 503].clone()
+    r()
+    assert int(r.error_word) == 0 and torch.equal(pages[last, 0, 501], row)

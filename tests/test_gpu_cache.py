@@ -331,3 +331,18 @@ def test_cache_calls_captured(sv):
                      (cache.free_count, ref.free_count), (calls[0].slots, calls_ref[0].slots), (pool, pool_ref)):
             assert torch.equal(x, y), r
     assert int(cache.error_word) == int(ref.error_word) == 0
+
+
+def test_empty_batch_and_slots_beyond_32_bits(sv):
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    slots, pos, ids, start, granted = sv.cache_extend(none, torch.zeros((0, 4), dtype=torch.int32, device="cuda"),
+                                                      i32([0]), i32([1]), 4, 3, extra=1)
+    assert slots.tolist() == [-1] * 3 and pos.tolist() == [0] * 3 and ids.tolist() == [-1] * 3 and start.tolist() == [0]
+    assert granted.numel() == 0
+    pages = (1 << 27) + 2
+    free = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    free[0] = 1 << 27
+    table = torch.full((1, 2), -1, dtype=torch.int32, device="cuda")
+    call = sv.CacheExtend(i32([0]), table, free, i32([1]), 64, 3, extra=3)
+    assert call()[0].tolist() == [(1 << 33) + k for k in range(3)] and int(call.error_word) == 0
+    assert table.tolist() == [[1 << 27, -1]]
