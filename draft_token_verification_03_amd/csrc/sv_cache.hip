@@ -331,7 +331,7 @@ __device__ __forceinline__ Kept kept_tokens(const CacheArgs &a, int b, bool &bad
     const int64_t want = (int64_t)a.accepted[b] + a.extra;
     const int keep = (int)min(max(want, (int64_t)0), (int64_t)held);
     if (!ended) {
-        bad = want != keep;
+        bad = want != keep && held > 0;  // what got no pages keeps nothing
         k.len = len + keep;
     }
     k.first = pages_of(a, k.len);

@@ -405,7 +405,8 @@ class PagedCache:
     the GPU: seq_len [B], block_table [B, max_blocks], free_list [num_pages]
     and free_count [1], reserved [B] (the tokens granted by the last extend)
     and one error_word for every call.  `extender` binds the call before a
-    forward pass, `committer` and `compactor` the calls after a verify step;
+    forward pass, `committer` and `compactor` the calls after a verify step,
+    in turn: an extend is committed before the next one;
     Verifier and TreeVerifier make the latter themselves when they are given
     the cache."""
 

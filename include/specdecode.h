@@ -127,7 +127,8 @@ int32_t spec_beam_reorder_paged(void *const *pools, int32_t n_pools, int32_t B, 
  * tokens reach beyond max_tokens is not granted any (SV_ERR_LENGTH).  A free
  * page outside [0, num_pages), or such an entry where a sequence's last page
  * is to be filled, sets SV_ERR_PAGE, and its tokens' slots are -1.
- * seq_len is left as it is: spec_cache_commit says what was kept.
+ * seq_len is left as it is: spec_cache_commit says what was kept, before the
+ * next extend (which would take pages for the same positions again).
  *   free_list [num_pages] int32;  free_count [1] in [0, num_pages]
  * B <= 2^20.  One kernel launch, two for more than 4096 tokens or 1024 sequences.
  */
@@ -150,7 +151,8 @@ int32_t spec_cache_extend(const int32_t *seq_len, const int32_t *new_len, int32_
  * given back are left as they are and mean nothing any more.
  *   page_start [B + 1] out: sum of the pages given back before b (the total last)
  *   seq_len_out may be seq_len, free_count_out may be free_count
- * k outside [0, reserved] is clamped, with SV_ERR_LENGTH; seq_len < 0,
+ * k outside [0, reserved] is clamped, with SV_ERR_LENGTH where anything was
+ * reserved (a sequence without its pages keeps nothing); seq_len < 0,
  * reserved < 0 or a sum above max_blocks * page_size set it too, give nothing
  * back and leave the length (0 for a finished one).  Pages that would make
  * the list longer than num_pages are not put there (SV_ERR_PAGES); a page

@@ -116,7 +116,7 @@ class CacheModel:
             if ended:
                 now = 0
             else:
-                bad |= keep != accepted[b] + extra
+                bad |= keep != accepted[b] + extra and r > 0
                 now = s + keep
             back += self.tables[b][self._blocks(now):self._blocks(s + r)]
             self.seq_len[b] = now

@@ -264,6 +264,39 @@ def test_decode_rounds_with_a_cache(sv, name, beta):
     assert sorted(cache.free_list.cpu().tolist()) == list(range(cache.num_pages))
 
 
+def test_rounds_when_pages_run_out(sv):
+    """Sequences without their pages keep nothing and lose nothing; once others
+    have ended they go on."""
+    w = WORKLOADS["C2"].sized(B=6, V=509)
+    cache = sv.PagedCache(w.B, 10, 13, 4)
+    inp = make_inputs(w, seed=3, device="cuda")
+    ext = cache.extender(w.B * (w.K + 1), extra=w.K + 1)
+    v = sv.Verifier(inp["target"], inp["draft"], inp["tokens"], inp["temperature"], cache=cache)
+    lens, lacked = [0] * w.B, False
+    for r in range(5):
+        slots, _, _, start, granted = ext()
+        granted, start, slots = granted.cpu().tolist(), start.cpu().tolist(), slots.cpu().tolist()
+        lacked |= 0 in granted
+        held = [s for s in slots if s >= 0]
+        assert len(set(held)) == len(held)
+        for b in range(w.B):
+            mine = slots[start[b]:start[b + 1]]
+            assert (min(mine) >= 0) if granted[b] else (max(mine) == -1)
+        acc = v(r)[0].cpu().tolist()
+        for b in range(w.B):
+            lens[b] += acc[b] + 1 if granted[b] else 0
+        assert cache.seq_len.cpu().tolist() == lens
+        assert int(cache.free_count) == 13 - sum(-(-n // 4) for n in lens)
+    assert lacked and int(cache.error_word) == sv.SV_ERR_PAGES
+    done = i32([1, 1, 1, 0, 0, 0])
+    cache.reserved.zero_()
+    cache.committer(i32([-1] * w.B), finished=done)()
+    # (the ended ones get no tokens: 13 pages hold three sequences of up to 16)
+    assert max(lens[3:]) + w.K + 1 <= 16
+    more = cache.extender(w.B * (w.K + 1), new_len=i32([-w.K - 1] * 3 + [0] * 3), extra=w.K + 1)
+    assert more()[4].cpu().tolist() == [0] * 3 + [w.K + 1] * 3
+
+
 def test_tree_rounds_with_a_cache(sv):
     """The same for trees: the accepted path's rows follow the root's."""
     w = WORKLOADS["C4"].sized(B=6, V=503)
