@@ -104,7 +104,9 @@ __device__ __forceinline__ int free_pages(const CacheArgs &a)
     return held;
 }
 
-constexpr int kTokens = 4;    // per thread where they have a launch of their own (1, 2, 8: 15.2, 13.9, 16.7 us against 13.7)
+// Tokens per thread where they have a launch of their own (1, 2, 8: 15.2, 13.9
+// and 16.7 us against 13.7 for a million).
+constexpr int kTokens = 4;
 constexpr int kStaged = 2048;  // sequences whose numbers a workgroup of it copies to LDS (64: 9.9 us against 11.0)
 
 // The last i in [lo, hi) with start[i] <= t (start[lo] <= t).

@@ -52,7 +52,7 @@ __device__ __forceinline__ BeamMoves<WM> beam_moves(const MoveArgs &a, int b)
 {
     const int lane = threadIdx.x & 63;
     int p = -1;
-    if (lane < a.W) p = a.parent[b * a.W + lane];
+    if (lane < a.W) p = a.parent[(int64_t)b * a.W + lane];
     if (p >= a.W) {
         move_error(a, SV_ERR_PARENT);
         p = -1;

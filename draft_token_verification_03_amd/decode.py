@@ -97,7 +97,7 @@ class BeamSelector(_Bound):
 
     logits [B, W, V] float32 or bfloat16, the last dimension contiguous, the
     others at any stride (expanded ones too); scores [B, W] float32, the beams'
-    cumulative log-probabilities (-inf: a dead beam, not read); temperature
+    cumulative log-probabilities (-inf: a dead beam, whose logits have no effect); temperature
     None (1), a float or a [B] float32 tensor; finished [B, W] int32: beams
     whose only continuation is `eos` at their score.  Each call returns
     (scores [B, M], parent [B, M], tokens [B, M], finished [B, M],
